@@ -8,6 +8,7 @@ missing the import of a function fails loudly -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -53,6 +54,11 @@ _SIGS = {
                                _I, _I, _F, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
     "mla_attn_split_kv_noalloc": (_I, [_P, _I64, _I, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P,
                                        _I, _P, _I, _I, _F, _P, _I, _P, _P, _P]),
+    "mla_paged_maps": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _P, _I64, _I] + [_P] * 6),
+    "mla_paged_cache_insert": (_I, [_P, _I64, _I, _P, _P, _P, _I, _I, _P]),
+    "mla_paged_attn_workspace_size": (ctypes.c_size_t, [_I, _I]),
+    "mla_paged_attn": (_I, [_P, _I64, _I, _P, _P, _I, _I, _P, _I, _I64, _P, _P, _P, _I, _P, _P,
+                            _F, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lock = threading.Lock()
@@ -315,6 +321,139 @@ def lse_merge_with_sink(o_part, lse_part, contrib_rows, o_out, lse_out, *, contr
         _ptr(_dev(contrib_rows, torch.int32, "contrib_rows")), T,
         _ptr(_dev(sink, torch.float32, "sink")), _ptr(_dev(o_out, torch.bfloat16, "o_out")),
         _ptr(_dev(lse_out, torch.float32, "lse_out")), _stream(stream)))
+
+
+# ------------------------------------------------------- the paged 8-bit cache
+def _on_device_of(fn):
+    """Run fn with its first tensor argument's device current, so that the
+    library's status word, stream and kernels are that device's; the other
+    tensors must lie there too."""
+    @functools.wraps(fn)
+    def call(first, *args, **kw):
+        tensors = [x for x in (first, *args, *kw.values(), *(kw.get("out") or {}).values())
+                   if isinstance(x, torch.Tensor)]
+        if not all(x.device == first.device for x in tensors):
+            raise ValueError("the tensors are on different devices")
+        if not first.is_cuda:
+            raise ValueError("the tensors must be on a CUDA device")
+        with torch.cuda.device(first.device):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _shaped(t, dtype, name, shape):
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return t
+
+
+def _paged_cache(cache, cache_exp):
+    _dev(cache, torch.uint8, "cache")
+    if cache.dim() != 3 or cache.shape[2] != DQK:
+        raise ValueError("cache must be [n_blocks, block_size, 576]")
+    _shaped(cache_exp, torch.uint8, "cache_exp", cache.shape[:1])
+    return cache.shape[0], cache.shape[1]
+
+
+def paged_maps_out(B, n_slots, device="cuda"):
+    """The output arrays of mla_paged_maps for B requests and n_slots entries."""
+    e = lambda n, dt: torch.empty(n, dtype=dt, device=device)
+    return dict(cu_seqlens=e(B + 1, torch.int32), slot_mapping=e(n_slots, torch.int64),
+                pos=e(n_slots, torch.int32), req=e(n_slots, torch.int32),
+                free_head=e(1, torch.int32))
+
+
+@_on_device_of
+def mla_paged_maps(ctx_len, new_len, free_blocks, block_table, *, block_size, n_blocks,
+                   n_slots=None, free_head=None, out=None, stream=None):
+    """Block tables and slot maps of a step from request lengths (int32 [B]):
+    request b, ctx_len[b] tokens in the cache, schedules new_len[b] more and
+    takes the blocks it lacks from free_blocks[free_head:] (int32), in request
+    order, into block_table [B, width] (in place).  Returns a dict (``out`` if
+    given, else for n_slots entries) of cu_seqlens [B + 1], slot_mapping
+    int64, pos and req int32 [n_slots] (-1 behind the last token) and free_head
+    [1], the count taken so far."""
+    _dev(ctx_len, torch.int32, "ctx_len")
+    B = ctx_len.numel()
+    _shaped(new_len, torch.int32, "new_len", (B,))
+    _dev(free_blocks, torch.int32, "free_blocks")
+    _dev(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, width]" % B)
+    if free_head is not None:
+        _shaped(free_head, torch.int32, "free_head", (1,))
+    if out is None:
+        if n_slots is None:
+            raise ValueError("n_slots or out is needed")
+        out = paged_maps_out(B, n_slots, ctx_len.device)
+    n_slots = out["slot_mapping"].numel()
+    _check(lib().mla_paged_maps(
+        _ptr(ctx_len), _ptr(new_len), B, int(block_size), int(n_blocks), _ptr(free_blocks),
+        free_blocks.numel(), _ptr(free_head), _ptr(block_table), block_table.shape[1], n_slots,
+        _ptr(_shaped(out["cu_seqlens"], torch.int32, "cu_seqlens", (B + 1,))),
+        _ptr(_shaped(out["slot_mapping"], torch.int64, "slot_mapping", (n_slots,))),
+        _ptr(_shaped(out["pos"], torch.int32, "pos", (n_slots,))),
+        _ptr(_shaped(out["req"], torch.int32, "req", (n_slots,))),
+        _ptr(_shaped(out["free_head"], torch.int32, "free_head", (1,))), _stream(stream)))
+    return out
+
+
+@_on_device_of
+def mla_paged_cache_insert(kv, slot_mapping, cache, cache_exp, *, stream=None):
+    """Write each token's latent KV row (kv [n, 576] bf16) to slot
+    slot_mapping[t] (int64, -1 skips) of the paged 8-bit cache, in place: cache
+    uint8 [n_blocks, block_size, 576] of E4M3 codes and cache_exp uint8
+    [n_blocks], the exponent (+ 127) of each block's scale.  The tokens of one
+    block stand side by side."""
+    nb, bs = _paged_cache(cache, cache_exp)
+    if not (kv.is_cuda and kv.dtype == torch.bfloat16 and kv.dim() == 2 and kv.shape[1] == DQK
+            and kv.stride(1) == 1):
+        raise ValueError("kv must be a CUDA bfloat16 [n, 576] tensor with contiguous rows")
+    n = kv.shape[0]
+    _check(lib().mla_paged_cache_insert(
+        _ptr(kv), kv.stride(0) if n > 1 else DQK, n,
+        _ptr(_shaped(slot_mapping, torch.int64, "slot_mapping", (n,))), _ptr(cache),
+        _ptr(cache_exp), nb, bs, _stream(stream)))
+
+
+def paged_attn_workspace(H, n_tokens, device="cuda"):
+    """A device buffer of the size mla_paged_attn needs (uint8, 256-byte
+    aligned by the caching allocator)."""
+    n = lib().mla_paged_attn_workspace_size(H, n_tokens)
+    return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
+
+
+@_on_device_of
+def mla_paged_attn(q, cache, cache_exp, block_table, pos, req, o_out, lse_out, *, softmax_scale,
+                   workspace, tokens=None, sink=None, kv_lo=None, kv_hi=None, stream=None):
+    """Attention of the listed entries over the paged 8-bit cache: entry i is
+    token tokens[i] (i when None) at position pos[i] of request req[i] (int32;
+    req -1 stands for no token), causal and within [kv_lo[i], kv_hi[i]] when
+    given.  q [T, H, 576] bf16 (tokens may be strided); writes the entries'
+    rows of o_out [T, H, 512] bf16 (sink applied once) and lse_out [T, H]."""
+    nb, bs = _paged_cache(cache, cache_exp)
+    if not (q.is_cuda and q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[2] == DQK
+            and q.stride(2) == 1 and (q.stride(1) == DQK or q.shape[1] == 1)):
+        raise ValueError("q must be a CUDA bfloat16 [T, H, 576] tensor with contiguous tokens")
+    T, H = q.shape[0], q.shape[1]
+    n = pos.numel()
+    _dev(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    if tokens is None and n > T:
+        raise ValueError("%d entries for %d tokens: give their tokens" % (n, T))
+    opt = lambda t, name: None if t is None else _shaped(t, torch.int32, name, (n,))
+    _check(lib().mla_paged_attn(
+        _ptr(q), q.stride(0) if T > 1 else H * DQK, H, _ptr(cache), _ptr(cache_exp), nb, bs,
+        _ptr(block_table), block_table.shape[0], block_table.shape[1],
+        _ptr(opt(tokens, "tokens")), _ptr(_shaped(pos, torch.int32, "pos", (n,))),
+        _ptr(_shaped(req, torch.int32, "req", (n,))), n, _ptr(opt(kv_lo, "kv_lo")),
+        _ptr(opt(kv_hi, "kv_hi")), float(softmax_scale),
+        None if sink is None else _ptr(_shaped(sink, torch.float32, "sink", (H,))), T,
+        _ptr(_shaped(o_out, torch.bfloat16, "o_out", (T, H, DV))),
+        _ptr(_shaped(lse_out, torch.float32, "lse_out", (T, H))),
+        _ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel(), _stream(stream)))
 
 
 def device_status(clear=True):

@@ -27,6 +27,10 @@ int *status_word();
     if (!(cond)) return ::cpmla::fail(CPMLA_ERR_ARG, __VA_ARGS__);        \
   } while (0)
 
+// Block sizes of the paged cache: 16, 32, 64 or 128 tokens.
+inline bool paged_block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+inline int paged_block_shift(int bs) { return bs == 16 ? 4 : bs == 32 ? 5 : bs == 64 ? 6 : 7; }
+
 // ---------------------------------------------------------------- device side
 #ifdef __CUDACC__
 

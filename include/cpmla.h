@@ -452,6 +452,118 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
                               float *lse_out, void *stream);
 
 /* --------------------------------------------------------------------------
+ * 2g. The paged 8-bit latent cache: a serving step in three calls (device)
+ *
+ * "[Core] Add MRV2 virtual-batch PCP for MLA", Summary (cache insertion by
+ * slot), and the fp8 cache dtype of "[Feature][PCP] Add DeepSeek-V4.1-Flash
+ * support"; the pages give neither a block format nor its arithmetic, which
+ * are the library's own.  The cache is a pool of blocks of `block_size`
+ * tokens (16, 32, 64 or 128), handed to requests in any order:
+ *   cache      uint8 [n_blocks, block_size, 576]: E4M3 codes of a token's 512
+ *              latent and 64 rope channels
+ *   cache_exp  uint8 [n_blocks]: the block's exponent e, stored as e + 127;
+ *              every value of the block is code * 2^e
+ *   block_table  int32 [B, table_stride]: block of request b's positions
+ *              block_size * i .. block_size * i + block_size - 1 at [b, i]
+ *   slot       block * block_size + position % block_size
+ * The scale of a block (its tokens share it, and MLA has one latent head) is
+ * a power of two, so that coding a token and lowering a block's codes when a
+ * larger token arrives are exact but for the E4M3 rounding itself.
+ *
+ * mla_paged_maps -- block tables and slot maps from request lengths: request
+ * b holds ctx_len[b] cached tokens and schedules new_len[b] more.  It takes
+ * ceil((ctx + new) / block_size) - ceil(ctx / block_size) blocks, in request
+ * order, from free_blocks[head], free_blocks[head + 1], ..., which are written
+ * to its table after the blocks it holds.  Scheduled token i of the batch
+ * (requests in order) of request b at position p gets
+ *   req[i] = b, pos[i] = p, slot_mapping[i] = its slot;
+ * entries behind the last token, up to n_slots, get -1 in all three.
+ *   ctx_len, new_len  int32 [B], >= 0
+ *   B                 1 .. 65536 (host)
+ *   block_size, n_blocks  as above (host)
+ *   free_blocks       int32 [n_free] blocks to hand out; n_free (host) >= 0
+ *   free_head         int32 [1]: entries of free_blocks that are taken
+ *                     already, or NULL for 0
+ *   block_table       int32 [B, table_stride] (host stride >= 1), read for
+ *                     the blocks a request holds, written for those it takes
+ *   n_slots           entries of the token arrays (host), >= 0
+ *   cu_seqlens        int32 [B + 1] output: first entry of each request
+ *   slot_mapping      int64 [n_slots], pos, req int32 [n_slots] outputs
+ *   free_head_out     int32 [1] output: free_head plus the blocks taken (not
+ *                     the same word as free_head)
+ * Recorded as CPMLA_ERR_INDEX in the status word, the rest of the batch
+ * unaffected: a negative length (taken as 0), more tokens than n_slots (those
+ * behind are dropped), a table or free list that is too short, or a block
+ * outside [0, n_blocks) in either (the tokens get slot -1).
+ *
+ * mla_paged_cache_insert -- tokens into their slots.  For a block, let N be
+ * the tokens of the call with a slot in it and e_N the least exponent >= -64
+ * with |x| <= 448 * 2^e_N for every finite channel x of N.  If N holds the
+ * block's row 0, the block starts anew and e = e_N; otherwise e = max(old e,
+ * e_N), and where that raises e the block's other rows are re-coded as
+ * E4M3(code * 2^(old e - e)).  Then every token of N is written as E4M3(x *
+ * 2^-e): nearest, ties to even; infinities saturate to +-448, NaN stays NaN.
+ *   kv               bf16 [n, 576], rows kv_token_stride elements apart (host,
+ *                    >= 576, a multiple of 8); 16-byte aligned
+ *   slot_mapping     int64 [n]; -1 skips the token, another slot outside the
+ *                    cache is skipped and recorded as CPMLA_ERR_INDEX
+ *   cache, cache_exp  the cache; cache 16-byte aligned
+ * The tokens of one block stand next to each other in the list, as
+ * mla_paged_maps lists them (those of two separate runs of one block would
+ * race for its exponent).  Of tokens with the same slot the last one is kept.
+ * Blocks that no token has a slot in are not touched.
+ *
+ * mla_paged_attn -- attention of listed tokens over the cache.  Entry i is
+ * global token g = tokens[i] (i itself when tokens is NULL) at position t =
+ * pos[i] of request b = req[i]; its keys are the positions j in 0..t, and in
+ * [kv_lo[i], kv_hi[i]] when those are given (a sliding window, a document or
+ * prefix of its own; lo > hi leaves none).  With k_j the 576 values of request
+ * b's position j and v_j the first 512 of them:
+ *   s_j = softmax_scale * q[g,h,:] . k_j,   L = ln sum_j exp(s_j)
+ *   o_out[g,h,:] = bf16( sum_j exp(s_j - L) v_j / (1 + exp(sink[h] - L)) )
+ *   lse_out[g,h] = L (without the sink); no key: 0 and -inf
+ * An entry with req[i] = -1 stands for no token and writes nothing, and rows
+ * of o_out / lse_out that no entry names are left as they were.  What lies in
+ * the cache at positions a row does not attend to (NaN codes included) does
+ * not reach it.
+ *   q, q_token_stride, H  as in section 2 (H > 64: a multiple of 64)
+ *   block_table      int32 [B, table_stride]; B, table_stride (host)
+ *   tokens, pos, req  int32 [n_tokens]; entries of one request side by side
+ *                    share its keys' loads (any order is right)
+ *   n_tokens         (host) >= 0; 0 is a no-op
+ *   softmax_scale, sink, T, o_out, lse_out  as in section 2e
+ *   workspace        device scratch of mla_paged_attn_workspace_size(H,
+ *                    n_tokens) bytes, 256-byte aligned, in no other use until
+ *                    this call's work on `stream` is done
+ * Recorded as CPMLA_ERR_INDEX and left out: an entry whose token lies outside
+ * [0, T), whose request is outside [-1, B) or whose position is negative or
+ * beyond its table row (nothing written for it), and a block outside [0,
+ * n_blocks) in a position that the entry attends to (its keys are skipped).
+ *
+ * All three: nothing is allocated, no host synchronisation, usable in stream
+ * capture.  Errors: CPMLA_ERR_ARG, CPMLA_ERR_UNSUPPORTED, CPMLA_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+int mla_paged_maps(const int32_t *ctx_len, const int32_t *new_len, int B, int block_size,
+                   int n_blocks, const int32_t *free_blocks, int n_free, const int32_t *free_head,
+                   int32_t *block_table, int64_t table_stride, int n_slots, int32_t *cu_seqlens,
+                   int64_t *slot_mapping, int32_t *pos, int32_t *req, int32_t *free_head_out,
+                   void *stream);
+
+int mla_paged_cache_insert(const void *kv, int64_t kv_token_stride, int n,
+                           const int64_t *slot_mapping, void *cache, uint8_t *cache_exp,
+                           int n_blocks, int block_size, void *stream);
+
+size_t mla_paged_attn_workspace_size(int H, int n_tokens);
+
+int mla_paged_attn(const void *q, int64_t q_token_stride, int H, const void *cache,
+                   const uint8_t *cache_exp, int n_blocks, int block_size,
+                   const int32_t *block_table, int B, int64_t table_stride, const int32_t *tokens,
+                   const int32_t *pos, const int32_t *req, int n_tokens, const int32_t *kv_lo,
+                   const int32_t *kv_hi, float softmax_scale, const float *sink, int T,
+                   void *o_out, float *lse_out, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/* --------------------------------------------------------------------------
  * 3. Global LSE merge + attention sink once + restore to global order (device)
  *
  * "[DeepSeekV4][PCP] ...", "Implementation summary" (merge LSE/output
