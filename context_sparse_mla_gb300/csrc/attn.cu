@@ -19,12 +19,6 @@
 #include "attn_common.cuh"
 
 namespace cpmla {
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -39,8 +33,6 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
-
-}  // namespace
 
 int attn_entry(bool sparse, const void *q, int64_t q_token_stride, int H, int kv_format,
                const void *kv, const void *kv_fp8, const float *kv_scale, const void *kv_rope,

@@ -167,6 +167,13 @@ __device__ __forceinline__ bool group_wait(uint64_t *bar, uint32_t parity, int t
   return *reinterpret_cast<volatile int *>(f) != 0;
 }
 
+// cuTensorMapEncodeTiled, or NULL when the driver has none (attn.cu).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // Options of attn_entry beyond the public entry points' arguments.
 struct AttnExtra {
   const int32_t *ent_lo = nullptr;  // per-row top-k window (sparse)

@@ -536,8 +536,8 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  *                    n_tokens) bytes, 256-byte aligned, in no other use until
  *                    this call's work on `stream` is done
  * Recorded as CPMLA_ERR_INDEX and left out: an entry whose token lies outside
- * [0, T), whose request is outside [-1, B) or whose position is negative or
- * beyond its table row (nothing written for it), and a block outside [0,
+ * [0, T), whose request is outside [-1, B) or whose position is negative, 2^30
+ * or more, or beyond its table row (nothing written for it), and a block outside [0,
  * n_blocks) in a position that the entry attends to (its keys are skipped).
  *
  * All three: nothing is allocated, no host synchronisation, usable in stream
