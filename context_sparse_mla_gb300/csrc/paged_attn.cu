@@ -35,9 +35,9 @@
 // group that is cut leaves normalised fp32 parts in the workspace, at most two
 // for each SM, and a third launch joins them in a fixed order.
 //
-// Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (chunks 0, 2 and 1,
-// 3), 3 loads (lane p: page p of a tile), 4-19 are four softmax warpgroups of
-// 16 rows (thread = key of the tile / channel of an O^T chunk).  Every wait is
+// Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (chunks 0, 2 and 1, 3),
+// 3 loads (lane p: page p of a tile), 4-11 do the
+// softmax, 12-15 the edges of a piece (q in, O out).  Every wait is
 // bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains its copies and
 // MMAs, frees TMEM and exits.
 #include <cmath>
@@ -72,6 +72,8 @@ struct PagedArgs {
   int n_cta;
   struct PgGroup *groups;
   int4 *start;      // [kPgMaxCtas + 1]: (group, head group, tile) a CTA starts at
+  int4 *joins;      // [1 + kPgMaxCtas]: a count, then (group, head group, first CTA, parts) of
+                    // what is cut
   float *o_part;    // [2 kPgMaxCtas][R][512]
   float *lse_part;  // [2 kPgMaxCtas][R], base 2
   int *status;
@@ -115,22 +117,31 @@ __device__ __forceinline__ long long pg_scan(long long v, int lane) {
 
 // Groups are runs of up to g entries of one request, cut at multiples of g.
 // A group's length in tile units is its tiles plus kPgUnitTail for each head
-// group; CTA c starts at unit floor(total c / n).
+// group; CTA c starts at unit floor(total c / n).  One CTA: the entries go by in
+// rounds through shared memory, and thread c looks up CTA c's start.
 __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedArgs a) {
-  __shared__ long long s_u[32], s_n[32];
+  __shared__ int s_b[kPgPlanThreads], s_lo[kPgPlanThreads], s_hi[kPgPlanThreads];
+  __shared__ long long s_u0[kPgPlanThreads];
+  __shared__ int s_nt[kPgPlanThreads];
+  __shared__ long long s_u[32];
+  __shared__ int s_n[32];
+  __shared__ int4 s_start[kPgMaxCtas + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int round = kPgPlanThreads / a.g * a.g;  // entries a round: no group crosses
   long long u_base = 0;
   int n_base = 0;
-  for (int r0 = 0; r0 < a.n; r0 += kPgPlanThreads) {
+  PgEntry nxt = pg_entry(a, tid < round ? tid : -1);
+  for (int r0 = 0; r0 < a.n; r0 += round) {
     const int i = r0 + tid;
-    const PgEntry e = pg_entry(a, i);
+    const PgEntry e = nxt;
+    if (r0 + round < a.n) nxt = pg_entry(a, tid < round ? i + round : -1);
     if (e.bad) record_status(a.status, CPMLA_ERR_INDEX);
-    bool start = e.ok;
-    if (start && i % a.g != 0) {
-      const PgEntry p = pg_entry(a, i - 1);
-      start = !p.ok || p.b != e.b;
-    }
+    s_b[tid] = e.ok ? e.b : -1;
+    s_lo[tid] = e.lo;
+    s_hi[tid] = e.hi;
+    __syncthreads();
     PgGroup m{};
+    const bool start = e.ok && (tid % a.g == 0 || s_b[tid - 1] != e.b);
     if (start) {
       m.first = i;
       m.req = e.b;
@@ -138,69 +149,104 @@ __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedA
       m.hi_max = -1;
       m.lo_max = -1;
       m.hi_min = INT32_MAX;
-      PgEntry x = e;
-      for (;;) {
-        if (x.lo <= x.hi) {
-          m.lo_min = min(m.lo_min, x.lo);
-          m.hi_max = max(m.hi_max, x.hi);
+      do {
+        const int lo = s_lo[tid + m.count], hi = s_hi[tid + m.count];
+        if (lo <= hi) {
+          m.lo_min = min(m.lo_min, lo);
+          m.hi_max = max(m.hi_max, hi);
         }
-        m.lo_max = max(m.lo_max, x.lo);
-        m.hi_min = min(m.hi_min, x.hi);
-        const int nx = i + ++m.count;
-        if (nx % a.g == 0) break;
-        x = pg_entry(a, nx);
-        if (!x.ok || x.b != e.b) break;
-      }
+        m.lo_max = max(m.lo_max, lo);
+        m.hi_min = min(m.hi_min, hi);
+        ++m.count;
+      } while ((tid + m.count) % a.g != 0 && s_b[tid + m.count] == e.b);
       if (m.hi_max >= 0) {
         m.t_lo = m.lo_min >> 7;
         m.n_tiles = (m.hi_max >> 7) - m.t_lo + 1;
       }
     }
     const long long units = start ? (long long)a.n_hg * (m.n_tiles + kPgUnitTail) : 0;
-    const long long su = pg_scan(units, lane), sn = pg_scan(start ? 1 : 0, lane);
-    __syncthreads();
+    const uint32_t starts = __ballot_sync(0xffffffffu, start);
+    const long long su = pg_scan(units, lane);
     if (lane == 31) {
       s_u[warp] = su;
-      s_n[warp] = sn;
+      s_n[warp] = __popc(starts);
     }
     __syncthreads();
     if (warp == 0) {
       s_u[lane] = pg_scan(s_u[lane], lane);
-      s_n[lane] = pg_scan(s_n[lane], lane);
+      s_n[lane] = (int)pg_scan(s_n[lane], lane);
     }
     __syncthreads();
     if (start) {
+      const int k = (warp ? s_n[warp - 1] : 0) + __popc(starts & ((1u << lane) - 1));
       m.u0 = u_base + (warp ? s_u[warp - 1] : 0) + su - units;
-      a.groups[n_base + (int)((warp ? s_n[warp - 1] : 0) + sn) - 1] = m;
+      a.groups[n_base + k] = m;
+      s_u0[k] = m.u0;
+      s_nt[k] = m.n_tiles;
     }
     u_base += s_u[31];
-    n_base += (int)s_n[31];
+    n_base += s_n[31];
+    __syncthreads();
   }
-  __syncthreads();
-  // starts: the CTA boundaries that fall into each group
+  // CTA c's start: the last group with u0 <= u
   const long long total = u_base;
-  long long want = total / kPgMinUnits;
-  const int n = total == 0 ? 0 : (int)(want < 1 ? 1 : (want < a.n_cta ? want : a.n_cta));
-  for (int g = tid; g < n_base; g += kPgPlanThreads) {
-    const PgGroup m = a.groups[g];
-    const int len = m.n_tiles + kPgUnitTail;
-    const long long u1 = m.u0 + (long long)a.n_hg * len;
-    for (long long c = (m.u0 * n + total - 1) / total; c < n; ++c) {
-      const long long u = total * c / n;
-      if (u >= u1) break;
-      int hg = (int)((u - m.u0) / len), off = (int)((u - m.u0) % len), gg = g;
-      if (off > 0 && off >= m.n_tiles) {  // in the group's tail: the next one
+  const int n = total == 0 ? 0 : (int)max(1ll, min((long long)a.n_cta, total / kPgMinUnits));
+  const bool one_round = a.n <= round;
+  if (tid <= kPgMaxCtas) {
+    int4 st = make_int4(n_base, 0, 0, 0);
+    if (tid < n) {
+      const long long u = total * tid / n;
+      int x = 0, y = n_base;
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if ((one_round ? s_u0[mid] : a.groups[mid].u0) <= u)
+          x = mid;
+        else
+          y = mid;
+      }
+      const int tiles = one_round ? s_nt[x] : a.groups[x].n_tiles, len = tiles + kPgUnitTail;
+      const int rel = (int)(u - (one_round ? s_u0[x] : a.groups[x].u0));
+      int hg = rel / len, off = rel - hg * len;
+      if (off > 0 && off >= tiles) {  // in the group's tail: the next one
         off = 0;
         if (++hg == a.n_hg) {
           hg = 0;
-          ++gg;
+          ++x;
         }
       }
-      a.start[c] = make_int4(gg, hg, off, 0);
+      st = make_int4(x, hg, off, 0);
     }
+    s_start[tid] = st;
+    a.start[tid] = st;
   }
-  for (int c = n + tid; c <= kPgMaxCtas; c += kPgPlanThreads)
-    a.start[c] = make_int4(n_base, 0, 0, 0);
+  __syncthreads();
+  // what is cut, by the first boundary inside it: CTAs c - 1, c, ... have parts
+  static_assert(kPgMaxCtas <= 5 * 32, "five warps look for cuts");
+  if (warp < 5) {
+    const int c = tid + 1;
+    int parts = 0;
+    int4 st = make_int4(0, 0, 0, 0);
+    if (c <= kPgMaxCtas) {
+      st = s_start[c];
+      const int4 p = s_start[c - 1];
+      if (st.z > 0 && !(p.x == st.x && p.y == st.y && p.z > 0)) {
+        parts = 2;
+        while (c + parts - 1 <= kPgMaxCtas) {
+          const int4 x = s_start[c + parts - 1];
+          if (x.x != st.x || x.y != st.y || x.z == 0) break;
+          ++parts;
+        }
+      }
+    }
+    const uint32_t b = __ballot_sync(0xffffffffu, parts > 0);
+    if (lane == 0) s_n[warp] = __popc(b);
+    named_bar_sync(1, 160);
+    int at = 0;
+    for (int x = 0; x < warp; ++x) at += s_n[x];
+    at += __popc(b & ((1u << lane) - 1));
+    if (parts > 0) a.joins[1 + at] = make_int4(st.x, st.y, c - 1, parts);
+    if (tid == 159) a.joins[0] = make_int4(at + (parts > 0 ? 1 : 0), 0, 0, 0);
+  }
 }
 
 // The pieces of a CTA: (group, head group) and a range of its tiles.
@@ -233,49 +279,66 @@ struct PgWalk {
 };
 
 // ------------------------------------------------------------- the attention
-constexpr int kPR = 64;                       // rows per CTA
-constexpr int kPWG = 4;                       // softmax warpgroups
-constexpr int kPRW = kPR / kPWG;              // rows per warpgroup
-constexpr int kPCtl = 4;                      // control warps
-constexpr int kPThreads = 32 * kPCtl + 128 * kPWG;
-constexpr int kPSlots = 7;                    // ring slots
-constexpr int kPSlot = 128 * 128;             // [128 keys x 128 channels]
-constexpr int kPRope = 128 * 64;
-constexpr int kPQBlock = 2 * kPR * 128;       // one 128-channel block of [h; l]
-constexpr int kPQBytes = 4 * kPQBlock + 2 * kPR * 64;
-constexpr int kPPBytes = 128 * kPR;           // one part of P^T
-constexpr int kPParts = 3;
-constexpr uint32_t kPTmemCols = 512;          // S^T 2 x 128, O^T 256
+constexpr int kPgThreads = 512;     // control, two softmax and one edge warpgroup
+constexpr int kPgSmWarps = 8;
+constexpr int kPgParts = 3;         // E5M2 parts of a weight
+constexpr int kPgSlot = 128 * 128;  // ring slot: [128 keys x 128 channels]
+constexpr int kPgRope = 128 * 64;   // [128 keys x 64], and q's [128 lanes x 64]
+constexpr uint32_t kPgTmemCols = 512;
 
+template <int R>
+struct PgCfg {
+  static constexpr int kPart = R * 128;  // one part of P: [R rows x 128 keys]
+  static constexpr int kP = kPgParts * kPart;
+  static constexpr int kSB = R == 64 ? 1 : 2;  // score buffers (TMEM: 4R + 128 kSB + 128 columns)
+  static constexpr int kFixed = kPgRope + 2 * kP + 2 * kPgRope;
+  static constexpr int kSlots = R == 64 ? 9 : (R == 32 ? 10 : 11);
+};
+
+template <int R>
 struct PgCtrl {
-  uint64_t full[kPSlots], empty[kPSlots];
-  uint64_t rope_full, rope_empty;
+  uint64_t full[PgCfg<R>::kSlots], empty[PgCfg<R>::kSlots];
+  uint64_t rope_full[2], rope_empty[2];
   uint64_t s_full[2], s_free[2];
-  uint64_t p_full, p_free;
-  uint64_t q_full, q_free;
+  uint64_t p_full[2], p_free[2];
+  // two each, for even and odd pieces: their waiters may be a piece behind
+  uint64_t q_full[2], st_full[2];  // a piece's q is in place; its m and l are in stat_m, stat_l
+  uint64_t q_free;
   uint64_t o_full, o_free;
   uint64_t drain[3];
   uint32_t tmem_base;
   int abort;
-  int bflag[kPWG][2];
-  int move[kPWG];        // tile + 1 of the last move of a reference
-  int rlo[kPR], rhi[kPR];
-  int tok[kPR];          // global token of a row, or -1
-  alignas(16) float qf[kPR];
-  alignas(16) float m_ref[kPR];
-  alignas(16) float alpha[kPR];
-  alignas(16) float inv[kPR];
-  float m_hi[kPR];
-  float red[kPWG][4][kPRW];
+  float qf[2][R];      // a piece's scale of q row r, times softmax scale and log2 e
+  float stat_m[2][R], stat_l[2][R];
+  alignas(16) float alpha[R];
+  // per edge warp: a row's output factor and its place in the output
+  alignas(16) float inv[4][R];
+  uint8_t *optr[4][R];
 };
-constexpr int kPSmem = 1024 + kPQBytes + kPParts * kPPBytes + kPRope + kPSlots * kPSlot +
-                       (int)sizeof(PgCtrl);
-static_assert(kPSmem <= 232448, "shared memory budget");
+template <int R>
+constexpr int pg_smem() {
+  return 1024 + PgCfg<R>::kFixed + PgCfg<R>::kSlots * kPgSlot + (int)sizeof(PgCtrl<R>);
+}
+static_assert(pg_smem<64>() <= 232448 && pg_smem<32>() <= 232448 && pg_smem<16>() <= 232448,
+              "shared memory budget");
 
-__device__ __forceinline__ void pg_drain(uint64_t *bar, uint32_t parity) {
+constexpr unsigned long long kPgDrainNs = 20ull * 1000 * 1000;
+__device__ __forceinline__ void pg_drain(uint64_t *bar, uint32_t parity,
+                                         unsigned long long limit_ns) {
   const unsigned long long t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < limit_ns) {
   }
+}
+// Bounded wait of a warp: lane 0 waits, the warp takes its result.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane,
+                                          volatile int *abort, int *status) {
+  int ok = 1;
+  if (lane == 0) ok = mbar_wait(bar, parity, abort, status) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 // Two fp16 less their upper bytes (an E5M2 each, cut): exact.
@@ -297,51 +360,81 @@ __device__ __forceinline__ uint2 split_q(float x0, float x1) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&b));
   return make_uint2(h, e4m3x2(16.f * (x0 - f.x), 16.f * (x1 - f.y)));
 }
+// The same of four channels (two words of bf16 pairs) times `down`.
+__device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, float down) {
+  const uint2 a = split_q(__uint_as_float(w0 << 16) * down,
+                          __uint_as_float(w0 & 0xFFFF0000u) * down);
+  const uint2 b = split_q(__uint_as_float(w1 << 16) * down,
+                          __uint_as_float(w1 & 0xFFFF0000u) * down);
+  return make_uint2(a.x | (b.x << 16), a.y | (b.y << 16));
+}
 // 2^e for the stored exponent e + 127
 __device__ __forceinline__ float pg_pow2(int stored) {
   return stored == 0 ? 5.877471754e-39f : __int_as_float(stored << 23);
 }
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+  tmem_st16(taddr, f);
+}
 
-__global__ void __launch_bounds__(kPThreads, 1)
+// Predicated stores (no branch each): only where `p` is not NULL.
+__device__ __forceinline__ void st_global_if(const void *p, void *dst, uint32_t v) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.u64 q, %0, 0;\n @q st.global.b32 [%1], %2;\n}\n" ::"l"(p),
+               "l"(dst), "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ void st_global_if(const void *p, void *dst, float v0, float v1) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u64 q, %0, 0;\n @q st.global.v2.f32 [%1], {%2, %3};\n}\n" ::"l"(p),
+      "l"(dst), "f"(v0), "f"(v1)
+      : "memory");
+}
+
+template <int R>
+__global__ void __launch_bounds__(kPgThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedArgs a,
                       const __grid_constant__ CUtensorMap tm_lat,
                       const __grid_constant__ CUtensorMap tm_rope) {
-  if (a.start[blockIdx.x].x == a.start[blockIdx.x + 1].x &&
-      a.start[blockIdx.x].y == a.start[blockIdx.x + 1].y &&
-      a.start[blockIdx.x].z == a.start[blockIdx.x + 1].z)
-    return;  // no tiles for this CTA
+  using Cfg = PgCfg<R>;
+  constexpr int NS = Cfg::kSlots, SB = Cfg::kSB;
+  {
+    const int4 s = a.start[blockIdx.x], e = a.start[blockIdx.x + 1];
+    if (s.x == e.x && s.y == e.y && s.z == e.z) return;  // no tiles for this CTA
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sQ = smem;                       // 4 blocks [128 rows x 128], rope [128 rows x 64]
-  uint8_t *sP = sQ + kPQBytes;              // three parts of P^T: [128 keys x 64 rows]
-  uint8_t *sRope = sP + kPParts * kPPBytes;  // [128 keys x 64]
-  uint8_t *sRing = sRope + kPRope;
-  PgCtrl &c = *reinterpret_cast<PgCtrl *>(sRing + kPSlots * kPSlot);
+  uint8_t *sQr = smem;                    // q's rope, [128 lanes x 64]
+  uint8_t *sP = sQr + kPgRope;            // two P of three parts
+  uint8_t *sRope = sP + 2 * Cfg::kP;      // two [128 keys x 64]
+  uint8_t *sRing = sRope + 2 * kPgRope;
+  PgCtrl<R> &c = *reinterpret_cast<PgCtrl<R> *>(sRing + NS * kPgSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < kPSlots; ++s) {
+    for (int s = 0; s < NS; ++s) {
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&c.rope_full[s], 1);
+      mbar_init(&c.rope_empty[s], 1);
       mbar_init(&c.s_full[s], 1);
-      mbar_init(&c.s_free[s], 128 * kPWG);
+      mbar_init(&c.s_free[s], kPgSmWarps);
+      mbar_init(&c.p_full[s], kPgSmWarps);
+      mbar_init(&c.p_free[s], 2);
+      mbar_init(&c.q_full[s], 4);
+      mbar_init(&c.st_full[s], kPgSmWarps);
     }
-    mbar_init(&c.rope_full, 1);
-    mbar_init(&c.rope_empty, 1);
-    mbar_init(&c.p_full, 128 * kPWG);
-    mbar_init(&c.p_free, 2);
-    mbar_init(&c.q_full, 128 * kPWG);
     mbar_init(&c.q_free, 1);
     mbar_init(&c.o_full, 2);
-    mbar_init(&c.o_free, 128 * kPWG);
+    mbar_init(&c.o_free, 4);
     for (int s = 0; s < 3; ++s) mbar_init(&c.drain[s], 1);
     c.abort = 0;
-    for (int g = 0; g < kPWG; ++g) c.move[g] = 0;
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc(&c.tmem_base, kPTmemCols);
+  if (warp == 0) tmem_alloc(&c.tmem_base, kPgTmemCols);
   if (warp == 3 && lane == 0) {
     tma_prefetch_desc(&tm_lat);
     tma_prefetch_desc(&tm_rope);
@@ -350,50 +443,52 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem_base;
-  const uint32_t tO = tmem + 4 * kPR;  // S^T buffer b at tmem + 2 R b; O^T chunk ch at tO + R ch
+  // columns: q [0, 128), S buffer b at 128 + 128 b, O^T chunk ch at tO + R ch
+  const uint32_t tS = tmem + 128, tO = tS + 128 * SB;
   volatile int *abort = &c.abort;
   PgWalk w(a, blockIdx.x);
 
   if (warp == 0) {
     // ------------------------------------------------------ score-GEMM issuer
     if (lane == 0) {
-      constexpr uint32_t id = idesc_e4m3(128, 2 * kPR, 0, 0);
-      const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024, kSwz128);
-      const uint64_t dqr = smem_desc(smem_u32(sQ + 4 * kPQBlock), 16, 512, kSwz64);
+      constexpr uint32_t id = idesc_e4m3(128, 128, 0, 0);
+      const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
       const uint64_t dr = smem_desc(smem_u32(sRing), 16, 1024, kSwz128);
       const uint64_t drr = smem_desc(smem_u32(sRope), 16, 512, kSwz64);
       bool ok = true;
       uint32_t j = 0, piece = 0, slot = 0, par = 0;
       while (ok && w.next(a)) {
         if (w.t1 <= w.t0) continue;
-        if (!mbar_wait(&c.q_full, piece & 1, abort, a.status)) {
+        if (!mbar_wait(&c.q_full[piece & 1], (piece >> 1) & 1, abort, a.status)) {
           ok = false;
           break;
         }
+        tc_fence_after();
         for (int t = w.t0; t < w.t1; ++t, ++j) {
-          const uint32_t b = j & 1;
-          if ((j >= 2 && !mbar_wait(&c.s_free[b], ((j >> 1) - 1) & 1, abort, a.status)) ||
-              !mbar_wait(&c.rope_full, j & 1, abort, a.status)) {
+          const uint32_t b = j % SB, rb = j & 1;
+          if (!mbar_wait(&c.rope_full[rb], (j >> 1) & 1, abort, a.status) ||
+              (j >= SB && !mbar_wait(&c.s_free[b], (j / SB - 1) & 1, abort, a.status))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t dS = tmem + b * 2 * kPR;
+          const uint32_t dS = tS + b * 128;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            mma_f8_ss(dS, drr + ((k * 32) >> 4), dqr + ((k * 32) >> 4), id, k);
-          mma_commit(&c.rope_empty);
+            mma_f8_ss(dS, dqr + ((k * 32) >> 4), drr + ((rb * kPgRope + k * 32) >> 4), id, k);
+          mma_commit(&c.rope_empty[rb]);
+#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             if (!mbar_wait(&c.full[slot], par, abort, a.status)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t da = dr + ((slot * kPSlot) >> 4), db = dq + ((ch * kPQBlock) >> 4);
+            const uint64_t db = dr + ((slot * kPgSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8_ss(dS, da + ((k * 32) >> 4), db + ((k * 32) >> 4), id, 1u);
-            if (++slot == kPSlots) {
+              mma_f8_ts(dS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id, 1u);
+            if (++slot == NS) {
               slot = 0;
               par ^= 1;
             }
@@ -406,17 +501,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       if (!ok) {
         mma_commit(&c.drain[0]);
-        pg_drain(&c.drain[0], 0);
+        pg_drain(&c.drain[0], 0, kWaitLimitNs);
       }
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------ PV-GEMM issuers
+    // (a thread gets an MMA out every 75-100 cycles, the tensor core takes 48).
+    // Loops here and at the edges stay rolled: all warps' code together is more
+    // than the instruction cache holds beside the softmax, and straight code
+    // that runs once a piece took 8 cycles an instruction.
     if (lane == 0) {
       const int me = warp - 1;
-      constexpr uint32_t id = idesc_e4m3_e5m2(128, kPR, 1, 1);
-      const uint64_t dp = smem_desc(smem_u32(sP), kPPBytes, 512, kSwz64);
-      const uint64_t dr = smem_desc(smem_u32(sRing), kPSlot, 1024, kSwz128);
+      constexpr uint32_t id = idesc_e4m3_e5m2(128, R, 1, 0);
+      const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024, kSwz128);
+      const uint64_t dr = smem_desc(smem_u32(sRing), kPgSlot, 1024, kSwz128);
       bool ok = true;
       uint32_t j = 0, piece = 0;
       while (ok && w.next(a)) {
@@ -426,34 +525,36 @@ __global__ void __launch_bounds__(kPThreads, 1)
           break;
         }
         for (int t = w.t0; t < w.t1; ++t, ++j) {
-          if (!mbar_wait(&c.p_full, j & 1, abort, a.status)) {
+          const uint32_t b = j & 1;
+          if (!mbar_wait(&c.p_full[b], (j >> 1) & 1, abort, a.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint64_t db = dp + ((b * Cfg::kP) >> 4);
+#pragma unroll 1
+          for (int ch = me; ch < 4; ch += 2) {
+            const uint32_t slot = (4 * j + ch) % NS;
+            const uint64_t da = dr + ((slot * kPgSlot) >> 4);
+            uint32_t acc = t > w.t0 ? 1u : 0u;
+#pragma unroll 1
+            for (uint32_t k = 0; k < 4; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int ch = me + 2 * i;
-            const uint32_t slot = (4 * j + ch) % kPSlots;
-            const uint64_t da = dr + ((slot * kPSlot) >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-              for (int y = 0; y < kPParts; ++y)
-                mma_f8_ss(tO + ch * kPR, da + ((k * 4096) >> 4),
-                          dp + ((y * kPPBytes + k * 32 * kPR) >> 4), id,
-                          (t > w.t0 || k > 0 || y > 0) ? 1u : 0u);
-            }
+              for (uint32_t y = 0; y < kPgParts; ++y) {
+                mma_f8_ss(tO + ch * R, da + ((k * 4096) >> 4),
+                          db + ((y * Cfg::kPart + k * 32) >> 4), id, acc);
+                acc = 1;
+              }
             mma_commit(&c.empty[slot]);
           }
-          mma_commit(&c.p_free);
+          mma_commit(&c.p_free[b]);
         }
         if (ok) mma_commit(&c.o_full);
         ++piece;
       }
       if (!ok) {
         mma_commit(&c.drain[1 + me]);
-        pg_drain(&c.drain[1 + me], 0);
+        pg_drain(&c.drain[1 + me], 0, kWaitLimitNs);
       }
     }
     __syncwarp();
@@ -478,11 +579,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int np = __popc(__ballot_sync(0xffffffffu, blk >= 0));
         const int y = blk << a.shift;
         for (int ch = -1; ch < 4; ++ch) {
-          uint64_t *fb = ch < 0 ? &c.rope_full : &c.full[slot];
+          uint64_t *fb = ch < 0 ? &c.rope_full[j & 1] : &c.full[slot];
           int good = 1;
           if (lane == 0) {
             if (ch < 0)
-              good = j < 1 || mbar_wait(&c.rope_empty, (j - 1) & 1, abort, a.status);
+              good = j < 2 || mbar_wait(&c.rope_empty[j & 1], ((j >> 1) - 1) & 1, abort, a.status);
             else
               good = use == 0 || mbar_wait(&c.empty[slot], (use - 1) & 1, abort, a.status);
             if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * bs * (ch < 0 ? 64 : 128)));
@@ -494,137 +595,59 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           if (blk >= 0) {
             if (ch < 0)
-              tma_load_2d(sRope + lane * bs * 64, &tm_rope, CPMLA_DV, y, fb);
+              tma_load_2d(sRope + (j & 1) * kPgRope + lane * bs * 64, &tm_rope, CPMLA_DV, y, fb);
             else
-              tma_load_2d(sRing + slot * kPSlot + lane * bs * 128, &tm_lat, ch * 128, y, fb);
+              tma_load_2d(sRing + slot * kPgSlot + lane * bs * 128, &tm_lat, ch * 128, y, fb);
           }
           __syncwarp();
           if (ch < 0) ++ropes;
-          if (ch >= 0 && ++slot == kPSlots) {
+          if (ch >= 0 && ++slot == NS) {
             slot = 0;
             ++use;
           }
         }
       }
     }
-    // the copies of the last uses have landed before the CTA exits
+    // giving up: the copies in flight have landed before the CTA exits
     if (!ok && lane == 0) {
-      const uint32_t n = use * kPSlots + slot;
-      for (uint32_t i = n > kPSlots ? n - kPSlots : 0; i < n; ++i)
-        pg_drain(&c.full[i % kPSlots], (i / kPSlots) & 1);
-      if (ropes > 0) pg_drain(&c.rope_full, (ropes - 1) & 1);
+      const uint32_t n = use * NS + slot;
+      for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
+        pg_drain(&c.full[i % NS], (i / NS) & 1, kPgDrainNs);
+      for (uint32_t i = ropes > 2 ? ropes - 2 : 0; i < ropes; ++i)
+        pg_drain(&c.rope_full[i & 1], (i >> 1) & 1, kPgDrainNs);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------ softmax, output
-    const int sw = warp - kPCtl, wg = sw >> 2, q4 = warp & 3;
-    const int t = q4 * 32 + lane;  // key of a tile, channel of an O^T chunk
+  } else if (warp >= 4 && warp < 4 + kPgSmWarps) {
+    // ------------------------------------------------------ softmax
+    // Of each 16 lanes of the scores the first 8 are the h parts of 8 q rows, the
+    // last 8 their l parts; a 16-lane load gives thread 4 r + c both parts of
+    // row r for keys 8 i + 2 c, 8 i + 2 c + 1 (i = 0..15), so a row belongs to four
+    // threads and its statistics need no other warp.  A warp that gives up
+    // goes on through the loop without waiting or writing, so that the barriers
+    // stay matched.
+    const int q4 = warp & 3, half = (warp - 4) >> 2, c4 = lane & 3;
+    const int r = q4 * 16 + half * 8 + (lane >> 2);
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const int cb = wg * kPRW;
-    const int bar = 1 + wg;
-    int seq = 0;
+    constexpr int kBar = 1, kBarN = 32 * kPgSmWarps;
+    const bool live = q4 * 16 < R;  // the warp has rows
     bool ok = true;
     uint32_t j = 0, piece = 0;
-    while (ok && w.next(a)) {
-      const int r_valid = w.m.count * a.hc, h0 = w.hg * a.hc;
+    while (w.next(a)) {
+      if (w.t1 <= w.t0) continue;
       const int32_t *row = a.table + (int64_t)w.m.req * a.stride;
-      const bool some = w.t1 > w.t0;
-      // this warpgroup's threads are done with the previous piece's rows (a
-      // warpgroup keeps to its own rows, so no barrier spans two of them)
-      named_bar_sync(bar, 128);
-      if (some && piece > 0 &&
-          !group_wait(&c.q_free, (piece - 1) & 1, t, bar, c.bflag[wg], seq, abort, a.status)) {
-        ok = false;
+      const bool mine = r < w.m.count * a.hc;
+      int lo = 1, hi = 0;
+      if (mine) {
+        const int i = w.m.first + r / a.hc;
+        lo = a.kv_lo ? max(a.kv_lo[i], 0) : 0;
+        hi = a.kv_hi ? min(a.kv_hi[i], a.pos[i]) : a.pos[i];
       }
-      // Q: warp sw takes rows 4 sw .. 4 sw + 3; channels 4 (lane + 32 i) ..
-      if (ok) {
-#pragma unroll 1
-        for (int rr = 0; rr < kPR / (4 * kPWG); ++rr) {
-          const int r = sw * (kPR / (4 * kPWG)) + rr;
-          const int l = r / a.hc, hh = r - l * a.hc;
-          const bool there = r < r_valid;
-          uint2 v[5];
-          int tok = -1;
-          if (there) {
-            const int i = w.m.first + l;
-            tok = a.tokens ? a.tokens[i] : i;
-            if (lane == 0) {
-              c.rlo[r] = a.kv_lo ? max(a.kv_lo[i], 0) : 0;
-              c.rhi[r] = a.kv_hi ? min(a.kv_hi[i], a.pos[i]) : a.pos[i];
-            }
-          } else if (lane == 0) {
-            c.rlo[r] = 1;
-            c.rhi[r] = 0;
-          }
-          const uint2 *src = reinterpret_cast<const uint2 *>(
-              a.q + (int64_t)(there ? tok : 0) * a.q_stride + (int64_t)(h0 + hh) * CPMLA_DQK);
-          uint32_t mx = 0;
-          bool fin = true;
-#pragma unroll
-          for (int i = 0; i < 5; ++i) {
-            v[i] = make_uint2(0, 0);
-            if (there && some && (i < 4 || lane < 16)) v[i] = __ldg(src + lane + 32 * i);
-            const uint32_t x[4] = {v[i].x << 16, v[i].x & 0xFFFF0000u, v[i].y << 16,
-                                   v[i].y & 0xFFFF0000u};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t ab = x[k] & 0x7FFFFFFFu;
-              if (ab >= 0x7F800000u)
-                fin = false;
-              else
-                mx = max(mx, ab);
-            }
-          }
-          mx = __reduce_max_sync(0xffffffffu, mx);
-          fin = __all_sync(0xffffffffu, fin);
-          // 2^ae: the largest channel in (224, 448] (ae >= -100: smaller rows
-          // keep fewer bits)
-          int ae = (int)(mx >> 23) - 127 - ((mx & 0x7FFFFFu) > 0x600000u ? 7 : 8);
-          ae = ae < -100 ? -100 : ae;
-          const float down = __int_as_float((127 - ae) << 23);
-          if (lane == 0) {
-            // a row with an infinite or NaN channel is NaN throughout
-            c.qf[r] = there ? (fin ? __int_as_float((127 + ae) << 23) * a.scale_log2 : NAN) : 0.f;
-            c.tok[r] = tok;
-            c.m_ref[r] = there ? -INFINITY : 1e30f;  // rows of no token get weight 0
-            c.m_hi[r] = -INFINITY;
-            c.alpha[r] = 1.f;
-          }
-          if (some) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-              if (i == 4 && lane >= 16) break;
-              const uint2 p0 = split_q(__uint_as_float(v[i].x << 16) * down,
-                                       __uint_as_float(v[i].x & 0xFFFF0000u) * down);
-              const uint2 p1 = split_q(__uint_as_float(v[i].y << 16) * down,
-                                       __uint_as_float(v[i].y & 0xFFFF0000u) * down);
-              const uint32_t hi = p0.x | (p1.x << 16), lo = p0.y | (p1.y << 16);
-              if (i < 4) {
-                // channels 128 i + 4 lane ..: block i, byte 4 lane of the row
-                const int off = i * kPQBlock + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                *reinterpret_cast<uint32_t *>(sQ + off + r * 128) = hi;
-                *reinterpret_cast<uint32_t *>(sQ + off + (kPR + r) * 128) = lo;
-              } else {
-                const int off =
-                    4 * kPQBlock + (((lane >> 2) ^ ((r >> 1) & 3)) << 4) + (lane & 3) * 4;
-                *reinterpret_cast<uint32_t *>(sQ + off + r * 64) = hi;
-                *reinterpret_cast<uint32_t *>(sQ + off + (kPR + r) * 64) = lo;
-              }
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        if (some) mbar_arrive(&c.q_full);
-      }
-      named_bar_sync(bar, 128);
-      if (!ok) break;
-
-      // key t of tile x: its block's stored exponent, or -1 when no row of the
-      // group may see it; the block of the next tile's key is fetched a tile
-      // ahead of its exponent
+      // group g of 16 keys of tile x (lane g and its copies): its block's stored
+      // exponent, or -1 where no row may look; the block of the next tile's
+      // group is fetched a tile ahead of its exponent
       auto block_at = [&](int x) {
-        const int p = (w.m.t_lo + x) * 128 + t;
-        if (x >= w.t1 || p < w.m.lo_min || p > w.m.hi_max) return -1;
+        const int p = (w.m.t_lo + x) * 128 + (lane & 7) * 16;
+        if (x >= w.t1 || p + 15 < w.m.lo_min || p > w.m.hi_max) return -1;
         const int blk = row[p >> a.shift];
         if (blk < 0 || blk >= a.n_blocks) {
           record_status(a.status, CPMLA_ERR_INDEX);
@@ -633,238 +656,372 @@ __global__ void __launch_bounds__(kPThreads, 1)
         return blk;
       };
       auto exp_of_block = [&](int blk) { return blk >= 0 ? min((int)__ldg(a.exp + blk), 254) : -1; };
-      float l_part[kPRW];
-#pragma unroll
-      for (int r = 0; r < kPRW; ++r) l_part[r] = 0.f;
       int e_cur = exp_of_block(block_at(w.t0));
       int b_nxt = block_at(w.t0 + 1);
+      if (ok) ok = warp_wait(&c.q_full[piece & 1], (piece >> 1) & 1, lane, abort, a.status);
+      const float qf = ok && mine ? c.qf[piece & 1][r] : 0.f;
+      float m_ref = -INFINITY, m_hi = -INFINITY, l = 0.f;
       for (int x = w.t0; x < w.t1; ++x, ++j) {
         const int e_nxt = exp_of_block(b_nxt);
         b_nxt = block_at(x + 2);
-        const uint32_t sb = j & 1;
-        if (!group_wait(&c.s_full[sb], (j >> 1) & 1, t, bar, c.bflag[wg], seq, abort, a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        float s[kPRW];
-        {
-          float lo[kPRW];
-          tmem_ld16(tmem + sb * 2 * kPR + lane_off + cb, s);
-          tmem_ld16(tmem + sb * 2 * kPR + lane_off + kPR + cb, lo);
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < kPRW; ++r) s[r] = fmaf(lo[r], 0.0625f, s[r]);
-        }
-        tc_fence_before();
-        mbar_arrive(&c.s_free[sb]);
-        const float kf = e_cur >= 0 ? pg_pow2(e_cur) : 0.f;
-        const float ku = (float)(e_cur - 127);
-        const int p = (w.m.t_lo + x) * 128 + t;
-        const bool open = p - t >= w.m.lo_max && p - t + 127 <= w.m.hi_min &&
+        const uint32_t sb = j % SB, pb = j & 1;
+        const int p0 = (w.m.t_lo + x) * 128;
+        const bool open = p0 >= w.m.lo_max && p0 + 127 <= w.m.hi_min &&
                           __all_sync(0xffffffffu, e_cur >= 0);
-        bool nan = false;
-        if (!open) {
-#pragma unroll
-          for (int r = 0; r < kPRW; ++r) nan |= s[r] != s[r];
-        }
-#pragma unroll
-        for (int r = 0; r < kPRW; r += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(&c.qf[cb + r]);
-          s[r] = fmaf(s[r] * kf, f.x, ku);
-          s[r + 1] = fmaf(s[r + 1] * kf, f.y, ku);
-          s[r + 2] = fmaf(s[r + 2] * kf, f.z, ku);
-          s[r + 3] = fmaf(s[r + 3] * kf, f.w, ku);
-        }
-        if (!open) {
-#pragma unroll
-          for (int r = 0; r < kPRW; ++r)
-            if (e_cur < 0 || p < c.rlo[cb + r] || p > c.rhi[cb + r]) s[r] = -INFINITY;
-          if (nan) {
-            // NaN codes in a key that not every row may see: weight zero times
-            // NaN would reach the others, so the key's values become zero (a
-            // row that does see it has a NaN weight)
-            bool found = false;
-            for (int ch = 0; ch < 4; ++ch) {
-              const uint32_t *kr = reinterpret_cast<const uint32_t *>(
-                  sRing + ((4 * j + ch) % kPSlots) * kPSlot + t * 128);
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t v = ~kr[i] & 0x7F7F7F7Fu;  // a zero byte: a NaN code
-                found |= ((v - 0x01010101u) & ~v & 0x80808080u) != 0;
-              }
-            }
-            if (found)
-              for (int ch = 0; ch < 4; ++ch)
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint4 *>(sRing + ((4 * j + ch) % kPSlots) * kPSlot + t * 128 +
-                                             i * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        {
-          float v[kPRW];
-#pragma unroll
-          for (int r = 0; r < kPRW; ++r) v[r] = s[r];
-          warp_transpose_reduce<kPRW, true>(v, lane);
-          if ((lane & 1) == 0) c.red[wg][q4][lane >> 1] = v[0];
-        }
-        named_bar_sync(bar, 128);
-        if (t < kPRW) {
-          const int r = cb + t;
-          const float tm = fmaxf(fmaxf(c.red[wg][0][t], c.red[wg][1][t]),
-                                 fmaxf(c.red[wg][2][t], c.red[wg][3][t]));
-          const float m_old = c.m_ref[r];
-          float m_new = m_old;
-          if (r < r_valid && tm > -INFINITY) {
-            const float m_hi = fmaxf(c.m_hi[r], tm);
-            c.m_hi[r] = m_hi;
-            const float d = tm - m_old;  // +inf at a row's first key
-            if (d > 15.75f)
-              m_new = tm - 10.f;
-            else if (d < 4.f)
-              m_new = fminf(m_old, fmaxf(tm, m_hi - 60.f) - 10.f);
-          }
-          c.alpha[r] = m_old == -INFINITY ? 0.f : fast_exp2(m_old - m_new);
-          c.m_ref[r] = m_new;
-          if (m_new != m_old) c.move[wg] = (int)j + 1;
-        }
-        named_bar_sync(bar, 128);
-        const bool moved = c.move[wg] == (int)j + 1;
-        if (moved) {
-#pragma unroll
-          for (int r = 0; r < kPRW; ++r)
-            l_part[r] = l_part[r] == 0.f ? 0.f : l_part[r] * c.alpha[cb + r];
-        }
-        // p as fp16 bits, split by cutting: an E5M2 is the upper byte of an fp16,
-        // so each part is the upper byte of what is left (nothing is negative);
-        // the last part is rounded
-        uint32_t part[kPParts][kPRW / 4];
-        const float kd = e_cur >= 0 ? pg_pow2(254 - e_cur) : 0.f;  // 2^-e
-#pragma unroll
-        for (int r = 0; r < kPRW; r += 4) {
-          const float4 m4 = *reinterpret_cast<const float4 *>(&c.m_ref[cb + r]);
-          const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-          float pv[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            pv[y] = fast_exp2(s[r + y] - (m[y] == -INFINITY ? 0.f : m[y]));
-            l_part[r + y] = fmaf(pv[y], kd, l_part[r + y]);
-          }
-          uint32_t a0 = pack_f16x2(pv[0], pv[1]), a1 = pack_f16x2(pv[2], pv[3]);
-#pragma unroll
-          for (int y = 0; y < kPParts; ++y) {
-            if (y == kPParts - 1) {
-              a0 += 0x00800080u;
-              a1 += 0x00800080u;
-            }
-            part[y][r / 4] = __byte_perm(a0, a1, 0x7531);
-            if (y < kPParts - 1) {
-              a0 = f16x2_minus_upper(a0);
-              a1 = f16x2_minus_upper(a1);
-            }
-          }
-        }
-        // the PV GEMM of the tile before is done with P^T and O^T
-        if (j >= 1 &&
-            !group_wait(&c.p_free, (j - 1) & 1, t, bar, c.bflag[wg], seq, abort, a.status)) {
-          ok = false;
-          break;
-        }
+        // 2^e and e of the key groups
+        const float kf = e_cur >= 0 ? pg_pow2(e_cur) : 1.f;
+        const float ku = (float)(e_cur - 127);
+        const uint32_t there = __ballot_sync(0xffffffffu, e_cur >= 0);
+        if (ok) ok = warp_wait(&c.s_full[sb], (j / SB) & 1, lane, abort, a.status);
         tc_fence_after();
-        if (moved && x > w.t0) {
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            float o[kPRW];
-            const uint32_t col = tO + lane_off + ch * kPR + cb;
-            tmem_ld16(col, o);
+        float s[32];
+        if (live && ok) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float v[32];
+            tmem_ld_16x256b_x8(tS + sb * 128 + lane_off + ((uint32_t)(half * 16) << 16) + g * 64, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int r = 0; r < kPRW; ++r) o[r] = o[r] == 0.f ? 0.f : o[r] * c.alpha[cb + r];
-            tmem_st16(col, o);
+            for (int i = 0; i < 8; ++i) {
+              s[g * 16 + 2 * i] = fmaf(v[4 * i + 2], 0.0625f, v[4 * i]);
+              s[g * 16 + 2 * i + 1] = fmaf(v[4 * i + 3], 0.0625f, v[4 * i + 1]);
+            }
           }
-          tmem_st_wait();
         }
-        uint8_t *pr = sP + t * kPR + ((wg ^ ((t >> 1) & 3)) << 4);
-#pragma unroll
-        for (int y = 0; y < kPParts; ++y)
-          *reinterpret_cast<uint4 *>(pr + y * kPPBytes) =
-              make_uint4(part[y][0], part[y][1], part[y][2], part[y][3]);
-        fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&c.p_full);
+        if (ok) warp_arrive(&c.s_free[sb], lane);
+        float um = -INFINITY;
+        if (live && ok) {
+          if (!open) {
+            // NaN codes in a key that not every row may see: weight zero times
+            // NaN would reach the others, so the key's values become zero (a
+            // row that does see it has a NaN weight).  A NaN code makes the
+            // scores of every row NaN, so any row's four threads know the keys;
+            // the warps share them out.
+            uint32_t nan = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) nan |= (uint32_t)(s[i] != s[i]) << i;
+            if (__any_sync(0xffffffffu, nan != 0)) {
+              const uint32_t n = 4 * j + (lane >> 3);  // this lane's chunk of the tile
+              // the copies are seen by this thread too (they landed long ago)
+              (void)mbar_wait(&c.full[n % NS], (n / NS) & 1, abort, a.status);
+              __syncwarp();
+              for (int k = q4 * 2 + half; k < 128; k += R / 8) {
+                const uint32_t nk = __shfl_sync(0xffffffffu, nan, (k >> 1) & 3);
+                if (((nk >> ((k >> 3) * 2 + (k & 1))) & 1) == 0) continue;
+                uint4 *kr = reinterpret_cast<uint4 *>(sRing + (n % NS) * kPgSlot + k * 128 +
+                                                      (lane & 7) * 16);
+                const uint4 v = *kr;
+                auto has = [](uint32_t u) {
+                  const uint32_t z = ~u & 0x7F7F7F7Fu;  // a zero byte: a NaN code
+                  return ((z - 0x01010101u) & ~z & 0x80808080u) != 0;
+                };
+                if (__any_sync(0xffffffffu, has(v.x) || has(v.y) || has(v.z) || has(v.w)))
+                  *kr = make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+          // u = t + e
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float f = qf * __shfl_sync(0xffffffffu, kf, g);
+            const float k0 = __shfl_sync(0xffffffffu, ku, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[4 * g + i] = fmaf(s[4 * g + i], f, k0);
+          }
+          if (!open) {
+#pragma unroll
+            for (int n = 0; n < 32; ++n) {
+              const int p = p0 + 8 * (n >> 1) + 2 * c4 + (n & 1);
+              if (((there >> (n >> 2)) & 1) == 0 || p < lo || p > hi) s[n] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < 32; ++n) um = fmaxf(um, s[n]);
+          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
+          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
+        }
+        // the reference follows the tile's maximum when it leaves the window
+        float m_new = m_ref;
+        if (mine && um > -INFINITY) {
+          m_hi = fmaxf(m_hi, um);
+          const float d = um - m_ref;  // +inf at a row's first key
+          if (d > 15.75f)
+            m_new = um - 10.f;
+          else if (d < 4.f)
+            m_new = fminf(m_ref, fmaxf(um, m_hi - 60.f) - 10.f);
+        }
+        const bool moved = named_bar_or(kBar, kBarN, m_new != m_ref);
+        if (moved) {
+          const float al = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+          l = l == 0.f ? 0.f : l * al;
+          if (x > w.t0) {
+            if (live && c4 == 0) c.alpha[r] = al;
+            named_bar_sync(kBar, kBarN);
+            // the PV GEMM of the tile before is done with O^T
+            if (ok) ok = warp_wait(&c.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1, lane, abort, a.status);
+            tc_fence_after();
+            if (ok) {
+#pragma unroll 1
+              for (int col = half * 2 * R; col < (half + 1) * 2 * R; col += 16) {
+                float o[16];
+                tmem_ld16(tO + lane_off + col, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  o[i] = o[i] == 0.f ? 0.f : o[i] * c.alpha[(col % R) + i];
+                tmem_st16(tO + lane_off + col, o);
+              }
+              tmem_st_wait();
+            }
+            named_bar_sync(kBar, kBarN);  // alpha is read
+          }
+          m_ref = m_new;
+        }
+        // this P buffer's last PV GEMM is done
+        if (ok && j >= 2) ok = warp_wait(&c.p_free[pb], ((j >> 1) - 1) & 1, lane, abort, a.status);
+        if (live && ok) {
+          const float mm = m_ref == -INFINITY ? 0.f : m_ref;
+          uint8_t *pr = sP + pb * Cfg::kP + r * 128 + 2 * c4;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            // p as fp16 bits, split by cutting: an E5M2 is the upper byte of an
+            // fp16, so each part is the upper byte of what is left (nothing is
+            // negative); the last part is rounded
+            float pv[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) pv[y] = fast_exp2(s[4 * g + y] - mm);
+            // 2^-e: the exponent field mirrored about that of 1
+            const float kd = __uint_as_float(
+                (254u << 23) - __float_as_uint(__shfl_sync(0xffffffffu, kf, g)));
+            l = fmaf((pv[0] + pv[1]) + (pv[2] + pv[3]), kd, l);
+            uint32_t a0 = pack_f16x2(pv[0], pv[1]), a1 = pack_f16x2(pv[2], pv[3]);
+#pragma unroll
+            for (int y = 0; y < kPgParts; ++y) {
+              if (y == kPgParts - 1) {
+                a0 += 0x00800080u;
+                a1 += 0x00800080u;
+              }
+              const uint32_t b4 = __byte_perm(a0, a1, 0x7531);
+              uint8_t *d = pr + y * Cfg::kPart + ((g ^ (r & 7)) << 4);
+              *reinterpret_cast<uint16_t *>(d) = (uint16_t)b4;
+              *reinterpret_cast<uint16_t *>(d + 8) = (uint16_t)(b4 >> 16);
+              if (y < kPgParts - 1) {
+                a0 = f16x2_minus_upper(a0);
+                a1 = f16x2_minus_upper(a1);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        if (ok) warp_arrive(&c.p_full[pb], lane);
         e_cur = e_nxt;
       }
-      if (!ok) break;
-      // ---------------------------------------------- this piece's output
-      const bool whole = w.whole();
-      if (some && !group_wait(&c.o_full, piece & 1, t, bar, c.bflag[wg], seq, abort, a.status)) {
-        ok = false;
-        break;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (live && c4 == 0) {
+        c.stat_m[piece & 1][r] = m_ref;
+        c.stat_l[piece & 1][r] = l;
       }
+      if (ok) warp_arrive(&c.st_full[piece & 1], lane);
+      ++piece;
+    }
+  } else if (warp >= 4 + kPgSmWarps) {
+    // ------------------------------------------------------ edges of a piece
+    // q into TMEM, ahead of its piece; O and LSE out, behind it
+    const int q4 = warp & 3, odd = lane & 1;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    bool ok = true;
+    // q of piece k.  TMEM lane 16 x + 8 part + y of this warp's 32 is part h or
+    // l of row 16 q4 + 8 x + y: thread 4 y + c reads 8 channels of rows y (x = 0,
+    // 1), 32 channels a step with its quad, and its 16-lane store puts both
+    // parts where they belong.  The last two steps, the rope, go to shared
+    // memory.  (The loops are kept short: see the MMA issuers.)
+    auto load_q = [&](const PgWalk &v, uint32_t k) {
+      const int r_valid = v.m.count * a.hc, y8 = lane >> 2, c4 = lane & 3;
+      const uint4 *src[2];
+      uint32_t mx[2] = {0, 0};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        // (rows of no token read the group's first one and are not used)
+        const int rr = q4 * 16 + 8 * x + y8 < r_valid ? q4 * 16 + 8 * x + y8 : 0;
+        const int n = v.m.first + rr / a.hc;
+        src[x] = reinterpret_cast<const uint4 *>(
+                     a.q + (int64_t)(a.tokens ? a.tokens[n] : n) * a.q_stride +
+                     (int64_t)(v.hg * a.hc + rr % a.hc) * CPMLA_DQK) +
+                 c4;
+      }
+      auto fetch = [&](int n, uint4 *w) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) w[x] = __ldg(src[x] + 4 * n);
+      };
+      if (q4 * 16 < R) {
+#pragma unroll 1
+        for (int n = 0; n < 18; n += 6) {
+          uint4 w[6][2];
+#pragma unroll
+          for (int i = 0; i < 6; ++i) fetch(n + i, w[i]);
+#pragma unroll
+          for (int i = 0; i < 6; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // the larger of two bf16 magnitudes in each half (NaN above all)
+              const uint32_t m01 = __vmaxu2(w[i][x].x & 0x7FFF7FFFu, w[i][x].y & 0x7FFF7FFFu);
+              const uint32_t m23 = __vmaxu2(w[i][x].z & 0x7FFF7FFFu, w[i][x].w & 0x7FFF7FFFu);
+              mx[x] = __vmaxu2(mx[x], __vmaxu2(m01, m23));
+            }
+        }
+      }
+      uint4 w[4][2];
+      if (q4 * 16 < R) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch(i, w[i]);
+      }
+      float down[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t m = max(mx[x] & 0xFFFFu, mx[x] >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // 2^ae brings the largest channel into (224, 448]; ae >= -60 (rows below
+        // keep fewer bits)
+        int ae = (int)(m >> 7) - 127 - ((m & 0x7Fu) > 0x60u ? 7 : 8);
+        ae = ae < -60 ? -60 : (ae > 120 ? 120 : ae);
+        down[x] = __int_as_float((127 - ae) << 23);
+        // a row with an infinite or NaN channel is NaN throughout
+        if (c4 == 0 && q4 * 16 < R)
+          c.qf[k & 1][q4 * 16 + 8 * x + y8] =
+              m >= 0x7F80u ? NAN : __int_as_float((127 + ae) << 23) * a.scale_log2;
+      }
+      // the score GEMMs of the piece before are done with q
+      if (k > 0) ok = warp_wait(&c.q_free, (k - 1) & 1, lane, abort, a.status);
+      if (!ok) return;
       tc_fence_after();
-      warp_transpose_reduce<kPRW, false>(l_part, lane);
-      if ((lane & 1) == 0) c.red[wg][q4][lane >> 1] = l_part[0];
-      named_bar_sync(bar, 128);
-      const int part = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-      if (t < kPRW) {
-        const int r = cb + t;
-        const float l = (c.red[wg][0][t] + c.red[wg][1][t]) + (c.red[wg][2][t] + c.red[wg][3][t]);
-        const float m = c.m_ref[r];
+      if (q4 * 16 < R) {
+#pragma unroll 1
+        for (int n = 0; n < 16; n += 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint2 p0 = split_q4(w[i][x].x, w[i][x].y, down[x]);
+              const uint2 p1 = split_q4(w[i][x].z, w[i][x].w, down[x]);
+              tmem_st_16x256b_x1(tmem + lane_off + ((uint32_t)(16 * x) << 16) + (n + i) * 8, p0.x,
+                                 p1.x, p0.y, p1.y);
+            }
+            fetch(min(n + i + 4, 17), w[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint2 p0 = split_q4(w[i][x].x, w[i][x].y, down[x]);
+            const uint2 p1 = split_q4(w[i][x].z, w[i][x].w, down[x]);
+            const int ln = q4 * 32 + 16 * x + y8, ck = i * 2 + (c4 >> 1);
+            uint8_t *d = sQr + ln * 64 + ((ck ^ ((ln >> 1) & 3)) << 4) + (c4 & 1) * 8;
+            *reinterpret_cast<uint2 *>(d) = make_uint2(p0.x, p1.x);
+            *reinterpret_cast<uint2 *>(d + 512) = make_uint2(p0.y, p1.y);  // lane + 8
+          }
+        tmem_st_wait();
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      warp_arrive(&c.q_full[k & 1], lane);
+    };
+    // O and LSE of piece k (k < 0: a piece without tiles)
+    auto put_out = [&](const PgWalk &v, int k) {
+      const bool some = k >= 0, whole = v.whole();
+      const int r_valid = v.m.count * a.hc, h0 = v.hg * a.hc;
+      const int part = 2 * blockIdx.x + (v.t0 == 0 ? 1 : 0);
+      if (some) {
+        ok = warp_wait(&c.st_full[k & 1], (k >> 1) & 1, lane, abort, a.status) &&
+             warp_wait(&c.o_full, k & 1, lane, abort, a.status);
+        if (!ok) return;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int rr = lane; rr < R; rr += 32) {
+        const float m = some ? c.stat_m[k & 1][rr] : -INFINITY;
+        const float l = some ? c.stat_l[k & 1][rr] : 0.f;
         const bool empty = m == -INFINITY && l == 0.f;  // l may be NaN
         const float l2 = empty ? -INFINITY : m + log2f(l);
         float f = empty ? 0.f : 1.f / l;
-        if (r < r_valid) {
+        uint8_t *optr = nullptr;
+        if (rr < r_valid) {
           if (whole) {
-            const int hh = h0 + r % a.hc;
+            const int hh = h0 + rr % a.hc, i = v.m.first + rr / a.hc;
             const float L = l2 * 0.69314718055994530942f;
             f *= sink_factor(a.sink, hh, L);
-            a.lse[(int64_t)c.tok[r] * a.H + hh] = L;
+            const int64_t orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
+            optr = reinterpret_cast<uint8_t *>(a.o + orow * CPMLA_DV);
+            if (q4 == 0) a.lse[orow] = L;
           } else {
-            a.lse_part[(int64_t)part * kPR + r] = l2;
+            const int64_t orow = (int64_t)part * R + rr;
+            optr = reinterpret_cast<uint8_t *>(a.o_part + orow * CPMLA_DV);
+            if (q4 == 0) a.lse_part[orow] = l2;
           }
         }
-        c.inv[r] = f;
+        c.inv[q4][rr] = f;
+        c.optr[q4][rr] = optr;
       }
-      named_bar_sync(bar, 128);
-      const bool odd = (lane & 1) != 0;
+      __syncwarp();
+      const int t = q4 * 32 + lane;
+      // 16 rows (columns of O^T) of a channel chunk at a time
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
-        float o[kPRW];
-        if (some) {
-          tmem_ld16(tO + lane_off + ch * kPR + cb, o);
-          tmem_ld_wait();
-        } else {
+      for (int cb = 0; cb < r_valid; cb += 16) {
+        float f[16];
+        uint8_t *p[8];  // rows cb + 2 y + odd
 #pragma unroll
-          for (int r = 0; r < kPRW; ++r) o[r] = 0.f;
-        }
+        for (int y = 0; y < 16; ++y) f[y] = c.inv[q4][cb + y];
 #pragma unroll
-        for (int r = 0; r < kPRW; ++r) {
-          const float f = c.inv[cb + r];
-          o[r] = f == 0.f ? 0.f : o[r] * f;
-        }
-        if (whole) {
-          // lane pairs trade one value: the even lane stores row r at channels
-          // t, t + 1, the odd lane row r + 1 at t - 1, t
+        for (int y = 0; y < 8; ++y) p[y] = c.optr[q4][cb + 2 * y + odd];
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          float o[16];
+          if (some) {
+            tmem_ld16(tO + lane_off + ch * R + cb, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-          for (int r = 0; r < kPRW; r += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[r] : o[r + 1], 1);
-            const int y = cb + r + (odd ? 1 : 0);
-            if (y < r_valid)
-              *reinterpret_cast<uint32_t *>(
-                  a.o + ((int64_t)c.tok[y] * a.H + h0 + y % a.hc) * CPMLA_DV + ch * 128 +
-                  (t & ~1)) = odd ? pack_bf16x2(got, o[r + 1]) : pack_bf16x2(o[r], got);
+            for (int y = 0; y < 16; ++y) o[y] = 0.f;
           }
-        } else {
 #pragma unroll
-          for (int r = 0; r < kPRW; ++r)
-            if (cb + r < r_valid)
-              a.o_part[((int64_t)part * kPR + cb + r) * CPMLA_DV + ch * 128 + t] = o[r];
+          for (int y = 0; y < 16; ++y) o[y] *= f[y];
+          // lane pairs trade one value: the even lane has row 2 y at channels
+          // t, t + 1, the odd lane row 2 y + 1 at t - 1, t
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[2 * y] : o[2 * y + 1], 1);
+            o[2 * y] = odd ? got : o[2 * y];
+            o[2 * y + 1] = odd ? o[2 * y + 1] : got;
+          }
+          if (whole) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              st_global_if(p[y], p[y] + ch * 256 + (t & ~1) * 2,
+                           pack_bf16x2(o[2 * y], o[2 * y + 1]));
+          } else {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              st_global_if(p[y], p[y] + ch * 512 + (t & ~1) * 4, o[2 * y], o[2 * y + 1]);
+          }
         }
       }
       tc_fence_before();
-      if (some) {
-        mbar_arrive(&c.o_free);
-        ++piece;
-      }
+      if (some) warp_arrive(&c.o_free, lane);
+      __syncwarp();
+    };
+    PgWalk prev = w;
+    int kq = 0, kp = -1;  // pieces with tiles so far; prev's number, -1 without tiles
+    for (bool have = false;; have = true) {
+      const bool more = w.next(a), some = more && w.t1 > w.t0;
+      if (some) load_q(w, kq);
+      if (have && ok) put_out(prev, kp);
+      if (!more || !ok) break;
+      prev = w;
+      kp = some ? kq++ : -1;
     }
   }
 
@@ -872,45 +1029,71 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kPTmemCols);
+    tmem_dealloc(tmem, kPgTmemCols);
   }
 }
 
 // ------------------------------------------------------------------ the join
-// Boundary c = blockIdx.x + 1 of the plan: if it is the first that cuts its
-// group, rows 4 blockIdx.y .. + 3 of the group are joined from their parts, in
-// CTA order.
+// Every row of every group in the plan's joins, a CTA a row: from its parts, in
+// CTA order, each weighted by 2^(its LSE - the largest); thread t has channels
+// 4 t .. 4 t + 3.  The parts were just written, so what takes time is the chain of
+// loads: the first eight parts' values are fetched beside their LSE.
+constexpr int kPgJoinCtas = 1024, kPgAhead = 8;
+template <int R>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
-  const int c0 = blockIdx.x + 1, t = threadIdx.x;
-  const int4 s = a.start[c0], p = a.start[c0 - 1];
-  if (s.z == 0 || (p.x == s.x && p.y == s.y && p.z > 0)) return;
-  const PgGroup m = a.groups[s.x];
-  int n = 1;  // parts: 2 c0 - 1, then 2 c0, 2 (c0 + 1), ...
-  while (c0 + n <= a.n_cta) {
-    const int4 x = a.start[c0 + n];
-    if (x.x != s.x || x.y != s.y || x.z == 0) break;
-    ++n;
-  }
-  for (int rr = 0; rr < 4; ++rr) {
-    const int r = blockIdx.y * 4 + rr;
-    if (r >= m.count * a.hc) return;
-    auto part = [&](int i) { return (int64_t)(i == 0 ? 2 * c0 - 1 : 2 * (c0 + i - 1)) * kPR + r; };
-    float mx = -INFINITY;
-    for (int i = 0; i <= n; ++i) mx = fmaxf(mx, a.lse_part[part(i)]);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i <= n; ++i) {
-      const float li = a.lse_part[part(i)];
-      if (li == -INFINITY) continue;
-      const float wt = exp2f(li - mx);
-      l += wt;
-      const float4 v = reinterpret_cast<const float4 *>(a.o_part + part(i) * CPMLA_DV)[t];
-      o.x = fmaf(wt, v.x, o.x);
-      o.y = fmaf(wt, v.y, o.y);
-      o.z = fmaf(wt, v.z, o.z);
-      o.w = fmaf(wt, v.w, o.w);
+  __shared__ float s_w[kPgMaxCtas];
+  const int t = threadIdx.x, lane = t & 31;
+  const int work = a.joins[0].x * R;
+  for (int x = blockIdx.x; x < work; x += gridDim.x) {
+    const int4 jn = a.joins[1 + x / R];
+    const int r = x % R, n = jn.w;
+    const PgGroup &m = a.groups[jn.x];
+    // part 0 is CTA jn.z's second, part i the first of CTA jn.z + i
+    auto at = [&](int i) { return (int64_t)(2 * (jn.z + i) + (i == 0 ? 1 : 0)) * R + r; };
+    auto value = [&](int i) {
+      return __ldcg(reinterpret_cast<const float4 *>(a.o_part + at(i) * CPMLA_DV) + t);
+    };
+    const int first = m.first, r_valid = m.count * a.hc;
+    if (r >= r_valid) continue;
+    float4 v[kPgAhead];
+#pragma unroll
+    for (int i = 0; i < kPgAhead; ++i)
+      v[i] = i < n ? value(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float p[(kPgMaxCtas + 31) / 32], mx = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < (kPgMaxCtas + 31) / 32; ++k) {
+      const int i = lane + 32 * k;
+      p[k] = i < n ? __ldcg(a.lse_part + at(i)) : -INFINITY;
+      mx = fmaxf(mx, p[k]);
     }
-    const int i = m.first + r / a.hc, h = s.y * a.hc + r % a.hc;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    __syncthreads();  // the row before is done with the weights
+#pragma unroll
+    for (int k = 0; k < (kPgMaxCtas + 31) / 32; ++k) {
+      const int i = lane + 32 * k;
+      const float wt = p[k] == -INFINITY ? 0.f : exp2f(p[k] - mx);  // NaN stays
+      if (i < kPgMaxCtas && t < 32) s_w[i] = wt;
+      l += wt;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += kPgAhead) {
+#pragma unroll
+      for (int i = 0; i < kPgAhead; ++i) {
+        const float wt = i0 + i < n ? s_w[i0 + i] : 0.f;
+        o.x = fmaf(wt, v[i].x, o.x);
+        o.y = fmaf(wt, v[i].y, o.y);
+        o.z = fmaf(wt, v[i].z, o.z);
+        o.w = fmaf(wt, v[i].w, o.w);
+      }
+#pragma unroll
+      for (int i = 0; i < kPgAhead; ++i)
+        if (i0 + kPgAhead + i < n) v[i] = value(i0 + kPgAhead + i);
+    }
+    const int i = first + r / a.hc, h = jn.y * a.hc + r % a.hc;
     const int64_t tok = a.tokens ? a.tokens[i] : i;
     const bool empty = mx == -INFINITY && l == 0.f;  // l may be NaN
     const float L = empty ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
@@ -923,16 +1106,40 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
 
 // Workspace sections, each 256-byte aligned.
 struct PgLayout {
-  size_t start, groups, o, lse, total;
+  size_t start, joins, groups, o, lse, total;
 };
-PgLayout pg_layout(int n) {
+PgLayout pg_layout(int n, int R) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PgLayout L{};
-  L.groups = up((kPgMaxCtas + 1) * sizeof(int4));
+  L.joins = up((kPgMaxCtas + 1) * sizeof(int4));
+  L.groups = L.joins + up((kPgMaxCtas + 1) * sizeof(int4));
   L.lse = L.groups + up((size_t)n * sizeof(PgGroup));
-  L.o = L.lse + up((size_t)2 * kPgMaxCtas * kPR * 4);
-  L.total = L.o + (size_t)2 * kPgMaxCtas * kPR * CPMLA_DV * 4;
+  L.o = L.lse + up((size_t)2 * kPgMaxCtas * R * 4);
+  L.total = L.o + (size_t)2 * kPgMaxCtas * R * CPMLA_DV * 4;
   return L;
+}
+
+// Rows per CTA.
+int pg_rows(int hc, int n_tokens, int B) {
+  if (n_tokens >= 2 * (int64_t)B || hc > 32) return 64;
+  return hc <= 16 ? 16 : 32;
+}
+
+template <int R>
+int launch_paged(const PagedArgs &a, const CUtensorMap &tm_lat, const CUtensorMap &tm_rope,
+                 cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<R>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, pg_smem<R>());
+  if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: set shared memory size");
+  paged_plan_kernel<<<1, kPgPlanThreads, 0, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: plan launch");
+  paged_attn_kernel<R><<<a.n_cta, kPgThreads, pg_smem<R>(), st>>>(a, tm_lat, tm_rope);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: launch");
+  if (a.n_cta > 1) {
+    paged_join_kernel<R><<<kPgJoinCtas, 128, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: join launch");
+  }
+  return CPMLA_OK;
 }
 
 }  // namespace
@@ -940,7 +1147,7 @@ PgLayout pg_layout(int n) {
 
 extern "C" size_t mla_paged_attn_workspace_size(int H, int n_tokens) {
   if (H < 1 || H > 128 || n_tokens < 0) return 0;
-  return cpmla::pg_layout(n_tokens).total;
+  return cpmla::pg_layout(n_tokens, 64).total;
 }
 
 extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, const void *cache,
@@ -1005,7 +1212,8 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
   a.lse = lse_out;
   a.status = status;
   a.hc = H <= 64 ? H : 64;
-  a.g = kPR / a.hc;
+  const int R = pg_rows(a.hc, n_tokens, B);
+  a.g = R / a.hc;
   a.n_hg = H / a.hc;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1013,8 +1221,9 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
   if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: device");
   a.n_cta = sms < kPgMaxCtas ? sms : kPgMaxCtas;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  const PgLayout L = pg_layout(n_tokens);
+  const PgLayout L = pg_layout(n_tokens, R);
   a.start = reinterpret_cast<int4 *>(ws + L.start);
+  a.joins = reinterpret_cast<int4 *>(ws + L.joins);
   a.groups = reinterpret_cast<PgGroup *>(ws + L.groups);
   a.lse_part = reinterpret_cast<float *>(ws + L.lse);
   a.o_part = reinterpret_cast<float *>(ws + L.o);
@@ -1038,15 +1247,7 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
       return fail(CPMLA_ERR_CUDA, "%s: tensor map encode failed (%d)", fn, (int)cr);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
-  if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: set shared memory size");
-  paged_plan_kernel<<<1, kPgPlanThreads, 0, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: plan launch");
-  paged_attn_kernel<<<a.n_cta, kPThreads, kPSmem, st>>>(a, tm[0], tm[1]);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: launch");
-  if (a.n_cta > 1) {
-    paged_join_kernel<<<dim3(a.n_cta - 1, kPR / 4), 128, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: join launch");
-  }
-  return CPMLA_OK;
+  return R == 64   ? launch_paged<64>(a, tm[0], tm[1], st)
+         : R == 32 ? launch_paged<32>(a, tm[0], tm[1], st)
+                   : launch_paged<16>(a, tm[0], tm[1], st);
 }
