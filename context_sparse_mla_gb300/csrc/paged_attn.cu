@@ -37,7 +37,7 @@
 //
 // Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (chunks 0, 2 and 1, 3),
 // 3 loads (lane p: page p of a tile), 4-11 do the
-// softmax, 12-15 the edges of a piece (q in, O out).  Every wait is
+// softmax and the output, 12-15 bring q in.  Every wait is
 // bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains its copies and
 // MMAs, frees TMEM and exits.
 #include <cmath>
@@ -49,7 +49,7 @@ namespace cpmla {
 namespace {
 
 constexpr int kPgMaxCtas = 160;   // at most one CTA per SM
-constexpr int kPgUnitTail = 2;    // a group's fixed cost, in tiles (plan)
+constexpr int kPgUnitTail = 3;    // a group's fixed cost, in tiles (plan)
 constexpr int kPgMinUnits = 4;    // tile units worth a CTA of its own
 constexpr int kPgPlanThreads = 1024;
 
@@ -72,8 +72,8 @@ struct PagedArgs {
   int n_cta;
   struct PgGroup *groups;
   int4 *start;      // [kPgMaxCtas + 1]: (group, head group, tile) a CTA starts at
-  int4 *joins;      // [1 + kPgMaxCtas]: a count, then (group, head group, first CTA, parts) of
-                    // what is cut
+  int4 *joins;      // a count, then two words for each group that is cut: (group, head group,
+                    // first CTA, parts), (first entry, rows, -, -)
   float *o_part;    // [2 kPgMaxCtas][R][512]
   float *lse_part;  // [2 kPgMaxCtas][R], base 2
   int *status;
@@ -244,7 +244,11 @@ __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedA
     int at = 0;
     for (int x = 0; x < warp; ++x) at += s_n[x];
     at += __popc(b & ((1u << lane) - 1));
-    if (parts > 0) a.joins[1 + at] = make_int4(st.x, st.y, c - 1, parts);
+    if (parts > 0) {
+      const PgGroup &m = a.groups[st.x];
+      a.joins[1 + 2 * at] = make_int4(st.x, st.y, c - 1, parts);
+      a.joins[2 + 2 * at] = make_int4(m.first, m.count * a.hc, 0, 0);
+    }
     if (tid == 159) a.joins[0] = make_int4(at + (parts > 0 ? 1 : 0), 0, 0, 0);
   }
 }
@@ -279,7 +283,7 @@ struct PgWalk {
 };
 
 // ------------------------------------------------------------- the attention
-constexpr int kPgThreads = 512;     // control, two softmax and one edge warpgroup
+constexpr int kPgThreads = 512;     // control, two softmax and one q warpgroup
 constexpr int kPgSmWarps = 8;
 constexpr int kPgParts = 3;         // E5M2 parts of a weight
 constexpr int kPgSlot = 128 * 128;  // ring slot: [128 keys x 128 channels]
@@ -301,19 +305,18 @@ struct PgCtrl {
   uint64_t rope_full[2], rope_empty[2];
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2], p_free[2];
-  // two each, for even and odd pieces: their waiters may be a piece behind
-  uint64_t q_full[2], st_full[2];  // a piece's q is in place; its m and l are in stat_m, stat_l
+  uint64_t q_full[2];  // q in place, for even and odd pieces: a waiter may be a piece behind
   uint64_t q_free;
   uint64_t o_full, o_free;
   uint64_t drain[3];
   uint32_t tmem_base;
   int abort;
   float qf[2][R];      // a piece's scale of q row r, times softmax scale and log2 e
-  float stat_m[2][R], stat_l[2][R];
+  float stat_m[R], stat_l[R];
   alignas(16) float alpha[R];
-  // per edge warp: a row's output factor and its place in the output
-  alignas(16) float inv[4][R];
-  uint8_t *optr[4][R];
+  // per softmax warp: a row's output factor and its place in the output
+  alignas(16) float inv[kPgSmWarps][R / 2];
+  uint8_t *optr[kPgSmWarps][R / 2];
 };
 template <int R>
 constexpr int pg_smem() {
@@ -425,11 +428,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(&c.p_full[s], kPgSmWarps);
       mbar_init(&c.p_free[s], 2);
       mbar_init(&c.q_full[s], 4);
-      mbar_init(&c.st_full[s], kPgSmWarps);
     }
     mbar_init(&c.q_free, 1);
     mbar_init(&c.o_full, 2);
-    mbar_init(&c.o_free, 4);
+    mbar_init(&c.o_free, kPgSmWarps);
     for (int s = 0; s < 3; ++s) mbar_init(&c.drain[s], 1);
     c.abort = 0;
     fence_mbar_init();
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     bool ok = true;
     uint32_t j = 0, piece = 0;
     while (w.next(a)) {
-      if (w.t1 <= w.t0) continue;
+      const bool some = w.t1 > w.t0;  // else a group that sees no key
       const int32_t *row = a.table + (int64_t)w.m.req * a.stride;
       const bool mine = r < w.m.count * a.hc;
       int lo = 1, hi = 0;
@@ -658,8 +660,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       auto exp_of_block = [&](int blk) { return blk >= 0 ? min((int)__ldg(a.exp + blk), 254) : -1; };
       int e_cur = exp_of_block(block_at(w.t0));
       int b_nxt = block_at(w.t0 + 1);
-      if (ok) ok = warp_wait(&c.q_full[piece & 1], (piece >> 1) & 1, lane, abort, a.status);
-      const float qf = ok && mine ? c.qf[piece & 1][r] : 0.f;
+      if (ok && some)
+        ok = warp_wait(&c.q_full[piece & 1], (piece >> 1) & 1, lane, abort, a.status);
+      const float qf = ok && some && mine ? c.qf[piece & 1][r] : 0.f;
       float m_ref = -INFINITY, m_hi = -INFINITY, l = 0.f;
       for (int x = w.t0; x < w.t1; ++x, ++j) {
         const int e_nxt = exp_of_block(b_nxt);
@@ -820,17 +823,101 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       }
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
+      // ---------------------------------------------- this piece's O and LSE
+      // A warp has a quarter of the channels (its TMEM lanes) and half of the rows.
       if (live && c4 == 0) {
-        c.stat_m[piece & 1][r] = m_ref;
-        c.stat_l[piece & 1][r] = l;
+        c.stat_m[r] = m_ref;
+        c.stat_l[r] = l;
       }
-      if (ok) warp_arrive(&c.st_full[piece & 1], lane);
-      ++piece;
+      named_bar_sync(kBar, kBarN);
+      if (ok && some) ok = warp_wait(&c.o_full, piece & 1, lane, abort, a.status);
+      tc_fence_after();
+      if (ok) {
+        constexpr int RH = R / 2, RS = RH < 16 ? RH : 16;
+        const int sw = warp - 4, r_valid = w.m.count * a.hc, h0 = w.hg * a.hc;
+        const bool whole = w.whole();
+        if (lane < RH) {
+          const int rr = half * RH + lane;
+          const float m = c.stat_m[rr], sl = c.stat_l[rr];
+          const bool empty = m == -INFINITY && sl == 0.f;  // l may be NaN
+          const float l2 = empty ? -INFINITY : m + log2f(sl);
+          float f = empty ? 0.f : 1.f / sl;
+          uint8_t *optr = nullptr;
+          if (rr < r_valid) {
+            if (whole) {
+              const int hh = h0 + rr % a.hc, i = w.m.first + rr / a.hc;
+              const float L = l2 * 0.69314718055994530942f;
+              f *= sink_factor(a.sink, hh, L);
+              const int64_t orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
+              optr = reinterpret_cast<uint8_t *>(a.o + orow * CPMLA_DV);
+              if (q4 == 0) a.lse[orow] = L;
+            } else {
+              const int64_t orow = (int64_t)(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * R + rr;
+              optr = reinterpret_cast<uint8_t *>(a.o_part + orow * CPMLA_DV);
+              if (q4 == 0) a.lse_part[orow] = l2;
+            }
+          }
+          c.inv[sw][lane] = f;
+          c.optr[sw][lane] = optr;
+        }
+        __syncwarp();
+        const int odd = lane & 1, t = q4 * 32 + lane;
+        // RS rows (columns of O^T) of a channel chunk at a time
+#pragma unroll 1
+        for (int cb = 0; cb < RH && half * RH + cb < r_valid; cb += RS) {
+          float f[RS];
+          uint8_t *p[RS / 2];  // rows cb + 2 y + odd
+#pragma unroll
+          for (int y = 0; y < RS; ++y) f[y] = c.inv[sw][cb + y];
+#pragma unroll
+          for (int y = 0; y < RS / 2; ++y) p[y] = c.optr[sw][cb + 2 * y + odd];
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            float o[RS];
+            if (some) {
+              const uint32_t col = tO + lane_off + ch * R + half * RH + cb;
+              if (RS == 16)
+                tmem_ld16(col, o);
+              else
+                tmem_ld8(col, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int y = 0; y < RS; ++y) o[y] = 0.f;
+            }
+#pragma unroll
+            for (int y = 0; y < RS; ++y) o[y] *= f[y];
+            // lane pairs trade one value: the even lane has row 2 y at channels
+            // t, t + 1, the odd lane row 2 y + 1 at t - 1, t
+#pragma unroll
+            for (int y = 0; y < RS / 2; ++y) {
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? o[2 * y] : o[2 * y + 1], 1);
+              o[2 * y] = odd ? got : o[2 * y];
+              o[2 * y + 1] = odd ? o[2 * y + 1] : got;
+            }
+            if (whole) {
+#pragma unroll
+              for (int y = 0; y < RS / 2; ++y)
+                st_global_if(p[y], p[y] + ch * 256 + (t & ~1) * 2,
+                             pack_bf16x2(o[2 * y], o[2 * y + 1]));
+            } else {
+#pragma unroll
+              for (int y = 0; y < RS / 2; ++y)
+                st_global_if(p[y], p[y] + ch * 512 + (t & ~1) * 4, o[2 * y], o[2 * y + 1]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (some) {
+        if (ok) warp_arrive(&c.o_free, lane);
+        ++piece;
+      }
+      named_bar_sync(kBar, kBarN);  // the statistics are read
     }
   } else if (warp >= 4 + kPgSmWarps) {
-    // ------------------------------------------------------ edges of a piece
-    // q into TMEM, ahead of its piece; O and LSE out, behind it
-    const int q4 = warp & 3, odd = lane & 1;
+    // ------------------------------------------------------ q into TMEM
+    const int q4 = warp & 3;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     bool ok = true;
     // q of piece k.  TMEM lane 16 x + 8 part + y of this warp's 32 is part h or
@@ -930,99 +1017,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       tc_fence_before();
       warp_arrive(&c.q_full[k & 1], lane);
     };
-    // O and LSE of piece k (k < 0: a piece without tiles)
-    auto put_out = [&](const PgWalk &v, int k) {
-      const bool some = k >= 0, whole = v.whole();
-      const int r_valid = v.m.count * a.hc, h0 = v.hg * a.hc;
-      const int part = 2 * blockIdx.x + (v.t0 == 0 ? 1 : 0);
-      if (some) {
-        ok = warp_wait(&c.st_full[k & 1], (k >> 1) & 1, lane, abort, a.status) &&
-             warp_wait(&c.o_full, k & 1, lane, abort, a.status);
-        if (!ok) return;
-        tc_fence_after();
-      }
-#pragma unroll
-      for (int rr = lane; rr < R; rr += 32) {
-        const float m = some ? c.stat_m[k & 1][rr] : -INFINITY;
-        const float l = some ? c.stat_l[k & 1][rr] : 0.f;
-        const bool empty = m == -INFINITY && l == 0.f;  // l may be NaN
-        const float l2 = empty ? -INFINITY : m + log2f(l);
-        float f = empty ? 0.f : 1.f / l;
-        uint8_t *optr = nullptr;
-        if (rr < r_valid) {
-          if (whole) {
-            const int hh = h0 + rr % a.hc, i = v.m.first + rr / a.hc;
-            const float L = l2 * 0.69314718055994530942f;
-            f *= sink_factor(a.sink, hh, L);
-            const int64_t orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
-            optr = reinterpret_cast<uint8_t *>(a.o + orow * CPMLA_DV);
-            if (q4 == 0) a.lse[orow] = L;
-          } else {
-            const int64_t orow = (int64_t)part * R + rr;
-            optr = reinterpret_cast<uint8_t *>(a.o_part + orow * CPMLA_DV);
-            if (q4 == 0) a.lse_part[orow] = l2;
-          }
-        }
-        c.inv[q4][rr] = f;
-        c.optr[q4][rr] = optr;
-      }
-      __syncwarp();
-      const int t = q4 * 32 + lane;
-      // 16 rows (columns of O^T) of a channel chunk at a time
-#pragma unroll 1
-      for (int cb = 0; cb < r_valid; cb += 16) {
-        float f[16];
-        uint8_t *p[8];  // rows cb + 2 y + odd
-#pragma unroll
-        for (int y = 0; y < 16; ++y) f[y] = c.inv[q4][cb + y];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) p[y] = c.optr[q4][cb + 2 * y + odd];
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float o[16];
-          if (some) {
-            tmem_ld16(tO + lane_off + ch * R + cb, o);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = 0.f;
-          }
-#pragma unroll
-          for (int y = 0; y < 16; ++y) o[y] *= f[y];
-          // lane pairs trade one value: the even lane has row 2 y at channels
-          // t, t + 1, the odd lane row 2 y + 1 at t - 1, t
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[2 * y] : o[2 * y + 1], 1);
-            o[2 * y] = odd ? got : o[2 * y];
-            o[2 * y + 1] = odd ? o[2 * y + 1] : got;
-          }
-          if (whole) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              st_global_if(p[y], p[y] + ch * 256 + (t & ~1) * 2,
-                           pack_bf16x2(o[2 * y], o[2 * y + 1]));
-          } else {
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              st_global_if(p[y], p[y] + ch * 512 + (t & ~1) * 4, o[2 * y], o[2 * y + 1]);
-          }
-        }
-      }
-      tc_fence_before();
-      if (some) warp_arrive(&c.o_free, lane);
-      __syncwarp();
-    };
-    PgWalk prev = w;
-    int kq = 0, kp = -1;  // pieces with tiles so far; prev's number, -1 without tiles
-    for (bool have = false;; have = true) {
-      const bool more = w.next(a), some = more && w.t1 > w.t0;
-      if (some) load_q(w, kq);
-      if (have && ok) put_out(prev, kp);
-      if (!more || !ok) break;
-      prev = w;
-      kp = some ? kq++ : -1;
-    }
+    for (uint32_t k = 0; ok && w.next(a);)
+      if (w.t1 > w.t0) load_q(w, k++);
   }
 
   tc_fence_before();
@@ -1038,23 +1034,23 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 // CTA order, each weighted by 2^(its LSE - the largest); thread t has channels
 // 4 t .. 4 t + 3.  The parts were just written, so what takes time is the chain of
 // loads: the first eight parts' values are fetched beside their LSE.
-constexpr int kPgJoinCtas = 1024, kPgAhead = 8;
+constexpr int kPgJoinCtas = 152 * 9, kPgAhead = 8;
 template <int R>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
   __shared__ float s_w[kPgMaxCtas];
   const int t = threadIdx.x, lane = t & 31;
   const int work = a.joins[0].x * R;
   for (int x = blockIdx.x; x < work; x += gridDim.x) {
-    const int4 jn = a.joins[1 + x / R];
+    const int4 jn = a.joins[1 + 2 * (x / R)], jg = a.joins[2 + 2 * (x / R)];
     const int r = x % R, n = jn.w;
-    const PgGroup &m = a.groups[jn.x];
     // part 0 is CTA jn.z's second, part i the first of CTA jn.z + i
     auto at = [&](int i) { return (int64_t)(2 * (jn.z + i) + (i == 0 ? 1 : 0)) * R + r; };
     auto value = [&](int i) {
       return __ldcg(reinterpret_cast<const float4 *>(a.o_part + at(i) * CPMLA_DV) + t);
     };
-    const int first = m.first, r_valid = m.count * a.hc;
-    if (r >= r_valid) continue;
+    if (r >= jg.y) continue;
+    const int i = jg.x + r / a.hc, h = jn.y * a.hc + r % a.hc;
+    const int64_t tok = a.tokens ? a.tokens[i] : i;
     float4 v[kPgAhead];
 #pragma unroll
     for (int i = 0; i < kPgAhead; ++i)
@@ -1093,8 +1089,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
       for (int i = 0; i < kPgAhead; ++i)
         if (i0 + kPgAhead + i < n) v[i] = value(i0 + kPgAhead + i);
     }
-    const int i = first + r / a.hc, h = jn.y * a.hc + r % a.hc;
-    const int64_t tok = a.tokens ? a.tokens[i] : i;
     const bool empty = mx == -INFINITY && l == 0.f;  // l may be NaN
     const float L = empty ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
     const float f = empty ? 0.f : sink_factor(a.sink, h, L) / l;
@@ -1112,7 +1106,7 @@ PgLayout pg_layout(int n, int R) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PgLayout L{};
   L.joins = up((kPgMaxCtas + 1) * sizeof(int4));
-  L.groups = L.joins + up((kPgMaxCtas + 1) * sizeof(int4));
+  L.groups = L.joins + up((2 * kPgMaxCtas + 1) * sizeof(int4));
   L.lse = L.groups + up((size_t)n * sizeof(PgGroup));
   L.o = L.lse + up((size_t)2 * kPgMaxCtas * R * 4);
   L.total = L.o + (size_t)2 * kPgMaxCtas * R * CPMLA_DV * 4;
