@@ -294,16 +294,23 @@ template <int R>
 struct PgCfg {
   static constexpr int kPart = R * 128;  // one part of P: [R rows x 128 keys]
   static constexpr int kP = kPgParts * kPart;
-  static constexpr int kSB = R == 64 ? 1 : 2;  // score buffers (TMEM: 4R + 128 kSB + 128 columns)
-  static constexpr int kFixed = kPgRope + 2 * kP + 2 * kPgRope;
-  static constexpr int kSlots = R == 64 ? 9 : (R == 32 ? 10 : 11);
+  // Parts of P side by side in one PV MMA, each with accumulators of its own (TMEM
+  // holds 4 R kWide + 256 columns): an MMA of N = 16, 32 or 64 takes 40, 40 or 48
+  // cycles, most of them for the 4 KB of keys, which N = 48 reads once for three.
+  static constexpr int kWide = R == 16 ? 3 : (R == 32 ? 2 : 1);
+  static constexpr int kOW = R * kWide;  // columns of an O^T chunk
+  // R = 64: one P buffer (the parts wait in registers for the PV GEMM before) and
+  // two ring slots more: a tile holds its slots for about 2.5 tile times
+  static constexpr int kPB = R == 64 ? 1 : 2;
+  static constexpr int kFixed = kPgRope + kPB * kP + kPgRope;
+  static constexpr int kSlots = R == 16 ? 12 : 11;
 };
 
 template <int R>
 struct PgCtrl {
   uint64_t full[PgCfg<R>::kSlots], empty[PgCfg<R>::kSlots];
-  uint64_t rope_full[2], rope_empty[2];
-  uint64_t s_full[2], s_free[2];
+  uint64_t rope_full, rope_empty;
+  uint64_t s_full, s_free;
   uint64_t p_full[2], p_free[2];
   uint64_t q_full[2];  // q in place, for even and odd pieces: a waiter may be a piece behind
   uint64_t q_free;
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                       const __grid_constant__ CUtensorMap tm_lat,
                       const __grid_constant__ CUtensorMap tm_rope) {
   using Cfg = PgCfg<R>;
-  constexpr int NS = Cfg::kSlots, SB = Cfg::kSB;
+  constexpr int NS = Cfg::kSlots, PB = Cfg::kPB;
   {
     const int4 s = a.start[blockIdx.x], e = a.start[blockIdx.x + 1];
     if (s.x == e.x && s.y == e.y && s.z == e.z) return;  // no tiles for this CTA
@@ -409,9 +416,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sQr = smem;                    // q's rope, [128 lanes x 64]
-  uint8_t *sP = sQr + kPgRope;            // two P of three parts
-  uint8_t *sRope = sP + 2 * Cfg::kP;      // two [128 keys x 64]
-  uint8_t *sRing = sRope + 2 * kPgRope;
+  uint8_t *sP = sQr + kPgRope;            // P of three parts, one or two
+  uint8_t *sRope = sP + PB * Cfg::kP;     // [128 keys x 64]
+  uint8_t *sRing = sRope + kPgRope;
   PgCtrl<R> &c = *reinterpret_cast<PgCtrl<R> *>(sRing + NS * kPgSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -421,14 +428,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(&c.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&c.rope_full[s], 1);
-      mbar_init(&c.rope_empty[s], 1);
-      mbar_init(&c.s_full[s], 1);
-      mbar_init(&c.s_free[s], kPgSmWarps);
       mbar_init(&c.p_full[s], kPgSmWarps);
       mbar_init(&c.p_free[s], 2);
       mbar_init(&c.q_full[s], 4);
     }
+    mbar_init(&c.rope_full, 1);
+    mbar_init(&c.rope_empty, 1);
+    mbar_init(&c.s_full, 1);
+    mbar_init(&c.s_free, kPgSmWarps);
     mbar_init(&c.q_free, 1);
     mbar_init(&c.o_full, 2);
     mbar_init(&c.o_free, kPgSmWarps);
@@ -445,8 +452,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem_base;
-  // columns: q [0, 128), S buffer b at 128 + 128 b, O^T chunk ch at tO + R ch
-  const uint32_t tS = tmem + 128, tO = tS + 128 * SB;
+  // columns: q [0, 128), S [128, 256), O^T chunk ch at tO + kOW ch
+  const uint32_t tS = tmem + 128, tO = tS + 128;
   volatile int *abort = &c.abort;
   PgWalk w(a, blockIdx.x);
 
@@ -467,18 +474,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         tc_fence_after();
         for (int t = w.t0; t < w.t1; ++t, ++j) {
-          const uint32_t b = j % SB, rb = j & 1;
-          if (!mbar_wait(&c.rope_full[rb], (j >> 1) & 1, abort, a.status) ||
-              (j >= SB && !mbar_wait(&c.s_free[b], (j / SB - 1) & 1, abort, a.status))) {
+          if (!mbar_wait(&c.rope_full, j & 1, abort, a.status) ||
+              (j >= 1 && !mbar_wait(&c.s_free, (j - 1) & 1, abort, a.status))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t dS = tS + b * 128;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            mma_f8_ss(dS, dqr + ((k * 32) >> 4), drr + ((rb * kPgRope + k * 32) >> 4), id, k);
-          mma_commit(&c.rope_empty[rb]);
+            mma_f8_ss(tS, dqr + ((k * 32) >> 4), drr + ((k * 32) >> 4), id, k);
+          mma_commit(&c.rope_empty);
 #pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             if (!mbar_wait(&c.full[slot], par, abort, a.status)) {
@@ -489,14 +494,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             const uint64_t db = dr + ((slot * kPgSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8_ts(dS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id, 1u);
+              mma_f8_ts(tS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id, 1u);
             if (++slot == NS) {
               slot = 0;
               par ^= 1;
             }
           }
           if (!ok) break;
-          mma_commit(&c.s_full[b]);
+          mma_commit(&c.s_full);
         }
         if (ok) mma_commit(&c.q_free);
         ++piece;
@@ -515,7 +520,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // that runs once a piece took 8 cycles an instruction.
     if (lane == 0) {
       const int me = warp - 1;
-      constexpr uint32_t id = idesc_e4m3_e5m2(128, R, 1, 0);
+      constexpr int W = Cfg::kWide, rest = kPgParts % W;  // parts a MMA, and in the last
+      constexpr uint32_t id = idesc_e4m3_e5m2(128, R * W, 1, 0);
+      constexpr uint32_t id_rest = idesc_e4m3_e5m2(128, R * (rest ? rest : W), 1, 0);
       const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024, kSwz128);
       const uint64_t dr = smem_desc(smem_u32(sRing), kPgSlot, 1024, kSwz128);
       bool ok = true;
@@ -527,8 +534,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           break;
         }
         for (int t = w.t0; t < w.t1; ++t, ++j) {
-          const uint32_t b = j & 1;
-          if (!mbar_wait(&c.p_full[b], (j >> 1) & 1, abort, a.status)) {
+          const uint32_t b = j % PB;
+          if (!mbar_wait(&c.p_full[b], (j / PB) & 1, abort, a.status)) {
             ok = false;
             break;
           }
@@ -542,9 +549,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll 1
             for (uint32_t k = 0; k < 4; ++k)
 #pragma unroll
-              for (uint32_t y = 0; y < kPgParts; ++y) {
-                mma_f8_ss(tO + ch * R, da + ((k * 4096) >> 4),
-                          db + ((y * Cfg::kPart + k * 32) >> 4), id, acc);
+              for (uint32_t y = 0; y < kPgParts; y += W) {
+                mma_f8_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4),
+                          db + ((y * Cfg::kPart + k * 32) >> 4), y + W <= kPgParts ? id : id_rest,
+                          acc);
                 acc = 1;
               }
             mma_commit(&c.empty[slot]);
@@ -581,11 +589,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int np = __popc(__ballot_sync(0xffffffffu, blk >= 0));
         const int y = blk << a.shift;
         for (int ch = -1; ch < 4; ++ch) {
-          uint64_t *fb = ch < 0 ? &c.rope_full[j & 1] : &c.full[slot];
+          uint64_t *fb = ch < 0 ? &c.rope_full : &c.full[slot];
           int good = 1;
           if (lane == 0) {
             if (ch < 0)
-              good = j < 2 || mbar_wait(&c.rope_empty[j & 1], ((j >> 1) - 1) & 1, abort, a.status);
+              good = j < 1 || mbar_wait(&c.rope_empty, (j - 1) & 1, abort, a.status);
             else
               good = use == 0 || mbar_wait(&c.empty[slot], (use - 1) & 1, abort, a.status);
             if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * bs * (ch < 0 ? 64 : 128)));
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           if (blk >= 0) {
             if (ch < 0)
-              tma_load_2d(sRope + (j & 1) * kPgRope + lane * bs * 64, &tm_rope, CPMLA_DV, y, fb);
+              tma_load_2d(sRope + lane * bs * 64, &tm_rope, CPMLA_DV, y, fb);
             else
               tma_load_2d(sRing + slot * kPgSlot + lane * bs * 128, &tm_lat, ch * 128, y, fb);
           }
@@ -615,8 +623,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       const uint32_t n = use * NS + slot;
       for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
         pg_drain(&c.full[i % NS], (i / NS) & 1, kPgDrainNs);
-      for (uint32_t i = ropes > 2 ? ropes - 2 : 0; i < ropes; ++i)
-        pg_drain(&c.rope_full[i & 1], (i >> 1) & 1, kPgDrainNs);
+      if (ropes > 0) pg_drain(&c.rope_full, (ropes - 1) & 1, kPgDrainNs);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + kPgSmWarps) {
@@ -667,7 +674,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       for (int x = w.t0; x < w.t1; ++x, ++j) {
         const int e_nxt = exp_of_block(b_nxt);
         b_nxt = block_at(x + 2);
-        const uint32_t sb = j % SB, pb = j & 1;
+        const uint32_t pb = j % PB;
         const int p0 = (w.m.t_lo + x) * 128;
         const bool open = p0 >= w.m.lo_max && p0 + 127 <= w.m.hi_min &&
                           __all_sync(0xffffffffu, e_cur >= 0);
@@ -675,14 +682,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const float kf = e_cur >= 0 ? pg_pow2(e_cur) : 1.f;
         const float ku = (float)(e_cur - 127);
         const uint32_t there = __ballot_sync(0xffffffffu, e_cur >= 0);
-        if (ok) ok = warp_wait(&c.s_full[sb], (j / SB) & 1, lane, abort, a.status);
+        if (ok) ok = warp_wait(&c.s_full, j & 1, lane, abort, a.status);
         tc_fence_after();
         float s[32];
         if (live && ok) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float v[32];
-            tmem_ld_16x256b_x8(tS + sb * 128 + lane_off + ((uint32_t)(half * 16) << 16) + g * 64, v);
+            tmem_ld_16x256b_x8(tS + lane_off + ((uint32_t)(half * 16) << 16) + g * 64, v);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
         }
         tc_fence_before();
-        if (ok) warp_arrive(&c.s_free[sb], lane);
+        if (ok) warp_arrive(&c.s_free, lane);
         float um = -INFINITY;
         if (live && ok) {
           if (!open) {
@@ -762,11 +769,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             if (live && c4 == 0) c.alpha[r] = al;
             named_bar_sync(kBar, kBarN);
             // the PV GEMM of the tile before is done with O^T
-            if (ok) ok = warp_wait(&c.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1, lane, abort, a.status);
+            if (ok) ok = warp_wait(&c.p_free[(j - 1) % PB], ((j - 1) / PB) & 1, lane, abort,
+                                   a.status);
             tc_fence_after();
             if (ok) {
 #pragma unroll 1
-              for (int col = half * 2 * R; col < (half + 1) * 2 * R; col += 16) {
+              for (int col = half * 2 * Cfg::kOW; col < (half + 1) * 2 * Cfg::kOW; col += 16) {
                 float o[16];
                 tmem_ld16(tO + lane_off + col, o);
                 tmem_ld_wait();
@@ -781,16 +789,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           m_ref = m_new;
         }
-        // this P buffer's last PV GEMM is done
-        if (ok && j >= 2) ok = warp_wait(&c.p_free[pb], ((j >> 1) - 1) & 1, lane, abort, a.status);
+        // p as fp16 bits, split by cutting: an E5M2 is the upper byte of an fp16, so
+        // each part is the upper byte of what is left (nothing is negative); the
+        // last part is rounded
+        uint32_t part[kPgParts][8];
         if (live && ok) {
           const float mm = m_ref == -INFINITY ? 0.f : m_ref;
-          uint8_t *pr = sP + pb * Cfg::kP + r * 128 + 2 * c4;
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            // p as fp16 bits, split by cutting: an E5M2 is the upper byte of an
-            // fp16, so each part is the upper byte of what is left (nothing is
-            // negative); the last part is rounded
             float pv[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) pv[y] = fast_exp2(s[4 * g + y] - mm);
@@ -805,14 +811,26 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 a0 += 0x00800080u;
                 a1 += 0x00800080u;
               }
-              const uint32_t b4 = __byte_perm(a0, a1, 0x7531);
-              uint8_t *d = pr + y * Cfg::kPart + ((g ^ (r & 7)) << 4);
-              *reinterpret_cast<uint16_t *>(d) = (uint16_t)b4;
-              *reinterpret_cast<uint16_t *>(d + 8) = (uint16_t)(b4 >> 16);
+              part[y][g] = __byte_perm(a0, a1, 0x7531);
               if (y < kPgParts - 1) {
                 a0 = f16x2_minus_upper(a0);
                 a1 = f16x2_minus_upper(a1);
               }
+            }
+          }
+        }
+        // this P buffer's last PV GEMM is done
+        if (ok && j >= PB)
+          ok = warp_wait(&c.p_free[pb], (j / PB - 1) & 1, lane, abort, a.status);
+        if (live && ok) {
+          uint8_t *pr = sP + pb * Cfg::kP + r * 128 + 2 * c4;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            uint8_t *d = pr + ((g ^ (r & 7)) << 4);
+#pragma unroll
+            for (int y = 0; y < kPgParts; ++y) {
+              *reinterpret_cast<uint16_t *>(d + y * Cfg::kPart) = (uint16_t)part[y][g];
+              *reinterpret_cast<uint16_t *>(d + y * Cfg::kPart + 8) = (uint16_t)(part[y][g] >> 16);
             }
           }
           fence_proxy_async_smem();
@@ -875,12 +893,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           for (int ch = 0; ch < 4; ++ch) {
             float o[RS];
             if (some) {
-              const uint32_t col = tO + lane_off + ch * R + half * RH + cb;
-              if (RS == 16)
-                tmem_ld16(col, o);
-              else
-                tmem_ld8(col, o);
+              float w3[Cfg::kWide][RS];
+#pragma unroll
+              for (int y = 0; y < Cfg::kWide; ++y) {
+                const uint32_t col = tO + lane_off + ch * Cfg::kOW + y * R + half * RH + cb;
+                if (RS == 16)
+                  tmem_ld16(col, w3[y]);
+                else
+                  tmem_ld8(col, w3[y]);
+              }
               tmem_ld_wait();
+#pragma unroll
+              for (int z = 0; z < RS; ++z) {
+                o[z] = w3[0][z];
+#pragma unroll
+                for (int y = 1; y < Cfg::kWide; ++y) o[z] += w3[y][z];
+              }
             } else {
 #pragma unroll
               for (int y = 0; y < RS; ++y) o[y] = 0.f;
@@ -965,7 +993,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) fetch(i, w[i]);
       }
-      float down[2];
+      float down[2], up[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         uint32_t m = max(mx[x] & 0xFFFFu, mx[x] >> 16);
@@ -977,15 +1005,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         ae = ae < -60 ? -60 : (ae > 120 ? 120 : ae);
         down[x] = __int_as_float((127 - ae) << 23);
         // a row with an infinite or NaN channel is NaN throughout
-        if (c4 == 0 && q4 * 16 < R)
-          c.qf[k & 1][q4 * 16 + 8 * x + y8] =
-              m >= 0x7F80u ? NAN : __int_as_float((127 + ae) << 23) * a.scale_log2;
+        up[x] = m >= 0x7F80u ? NAN : __int_as_float((127 + ae) << 23) * a.scale_log2;
       }
-      // the score GEMMs of the piece before are done with q
+      // the score GEMMs of the piece before are done with q (and so the softmax is
+      // past the start of that piece, and done with the scales of the one before)
       if (k > 0) ok = warp_wait(&c.q_free, (k - 1) & 1, lane, abort, a.status);
       if (!ok) return;
       tc_fence_after();
       if (q4 * 16 < R) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (c4 == 0) c.qf[k & 1][q4 * 16 + 8 * x + y8] = up[x];
 #pragma unroll 1
         for (int n = 0; n < 16; n += 4) {
 #pragma unroll
