@@ -36,7 +36,7 @@
 // for each SM, and a third launch joins them in a fixed order.
 //
 // Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (chunks 0, 2 and 1, 3),
-// 3 loads (lane p: page p of a tile), 4-11 do the
+// 3 loads, 4-11 do the
 // softmax and the output, 12-15 bring q in.  Every wait is
 // bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains its copies and
 // MMAs, frees TMEM and exits.
@@ -382,13 +382,6 @@ __device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, float down) 
 __device__ __forceinline__ float pg_pow2(int stored) {
   return stored == 0 ? 5.877471754e-39f : __int_as_float(stored << 23);
 }
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
-  float f[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
-  tmem_st16(taddr, f);
-}
-
 // Predicated stores (no branch each): only where `p` is not NULL.
 __device__ __forceinline__ void st_global_if(const void *p, void *dst, uint32_t v) {
   asm volatile("{\n .reg .pred q;\n setp.ne.u64 q, %0, 0;\n @q st.global.b32 [%1], %2;\n}\n" ::"l"(p),
@@ -459,57 +452,62 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ score-GEMM issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_e4m3(128, 128, 0, 0);
-      const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
-      const uint64_t dr = smem_desc(smem_u32(sRing), 16, 1024, kSwz128);
-      const uint64_t drr = smem_desc(smem_u32(sRope), 16, 512, kSwz64);
-      bool ok = true;
-      uint32_t j = 0, piece = 0, slot = 0, par = 0;
-      while (ok && w.next(a)) {
-        if (w.t1 <= w.t0) continue;
-        if (!mbar_wait(&c.q_full[piece & 1], (piece >> 1) & 1, abort, a.status)) {
+    // The lanes wait side by side for what a tile needs (a wait that is over takes
+    // 100-200 cycles all the same; one after another they took as long as the
+    // MMAs), then lane 0 issues.
+    constexpr uint32_t id = idesc_e4m3(128, 128, 0, 0);
+    const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
+    const uint64_t dr = smem_desc(smem_u32(sRing), 16, 1024, kSwz128);
+    const uint64_t drr = smem_desc(smem_u32(sRope), 16, 512, kSwz64);
+    bool ok = true;
+    uint32_t j = 0, piece = 0;
+    while (ok && w.next(a)) {
+      if (w.t1 <= w.t0) continue;
+      for (int t = w.t0; t < w.t1; ++t, ++j) {
+        // lanes 0-3: the latent chunks, 4: the rope, 5: the scores' buffer, 6: q
+        uint64_t *bar = nullptr;
+        uint32_t par = j;
+        if (lane < 4) {
+          bar = &c.full[(4 * j + lane) % NS];
+          par = (4 * j + lane) / NS;
+        } else if (lane == 4) {
+          bar = &c.rope_full;
+        } else if (lane == 5 && j > 0) {
+          bar = &c.s_free;
+          par = j - 1;
+        } else if (lane == 6 && t == w.t0) {
+          bar = &c.q_full[piece & 1];
+          par = piece >> 1;
+        }
+        const bool good = !bar || mbar_wait(bar, par & 1, abort, a.status);
+        if (!__all_sync(0xffffffffu, good)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        for (int t = w.t0; t < w.t1; ++t, ++j) {
-          if (!mbar_wait(&c.rope_full, j & 1, abort, a.status) ||
-              (j >= 1 && !mbar_wait(&c.s_free, (j - 1) & 1, abort, a.status))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (lane == 0) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma_f8_ss(tS, dqr + ((k * 32) >> 4), drr + ((k * 32) >> 4), id, k);
-          mma_commit(&c.rope_empty);
-#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
-            if (!mbar_wait(&c.full[slot], par, abort, a.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t db = dr + ((slot * kPgSlot) >> 4);
+            const uint64_t db = dr + (((4 * j + ch) % NS * kPgSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8_ts(tS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id, 1u);
-            if (++slot == NS) {
-              slot = 0;
-              par ^= 1;
-            }
+              mma_f8_ts(tS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id,
+                        (ch | k) != 0 ? 1u : 0u);
           }
-          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            mma_f8_ss(tS, dqr + ((k * 32) >> 4), drr + ((k * 32) >> 4), id, 1u);
           mma_commit(&c.s_full);
+          mma_commit(&c.rope_empty);
+          if (t + 1 == w.t1) mma_commit(&c.q_free);
         }
-        if (ok) mma_commit(&c.q_free);
-        ++piece;
+        __syncwarp();
       }
-      if (!ok) {
-        mma_commit(&c.drain[0]);
-        pg_drain(&c.drain[0], 0, kWaitLimitNs);
-      }
+      ++piece;
+    }
+    if (!ok && lane == 0) {
+      mma_commit(&c.drain[0]);
+      pg_drain(&c.drain[0], 0, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
@@ -570,58 +568,61 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------ loads
-    // lane p < 128 / block_size: page p of the tile
-    const int bs = 1 << a.shift, ppt = 128 >> a.shift;
+    // Lane 5 p + x: chunk x (4: the rope) of page p of a tile, and of page p + 4
+    // where a tile has eight.  Chunks 0 and 1, then 2 and 3, then the rope: one
+    // instruction issues the boxes of all lanes concerned, about 80 cycles each
+    // (box after box, each behind its own wait, a tile's took 4200 cycles and
+    // bounded the kernel; all at once, the first slots would wait for the last).
+    const int bs = 1 << a.shift, ppt = 128 >> a.shift, pg = lane / 5, kd = lane - 5 * pg;
+    const bool act = pg < (ppt < 4 ? ppt : 4), arm = lane < 5;
+    const uint32_t row_bytes = kd == 4 ? 64 : 128;
+    const CUtensorMap *tm = kd == 4 ? &tm_rope : &tm_lat;
     bool ok = true;
-    uint32_t j = 0, slot = 0, use = 0, ropes = 0;
+    uint32_t j = 0, items = 0, ropes = 0;
     while (ok && w.next(a)) {
       const int32_t *row = a.table + (int64_t)w.m.req * a.stride;
-      auto page = [&](int t) {
-        const int p0 = (w.m.t_lo + t) * 128 + lane * bs;
-        if (lane >= ppt || t >= w.t1 || p0 > w.m.hi_max || p0 + bs <= w.m.lo_min) return -1;
+      auto page = [&](int t, int p) {
+        const int p0 = (w.m.t_lo + t) * 128 + p * bs;
+        if (!act || p >= ppt || t >= w.t1 || p0 > w.m.hi_max || p0 + bs <= w.m.lo_min) return -1;
         const int blk = row[p0 >> a.shift];
         return blk >= 0 && blk < a.n_blocks ? blk : -1;
       };
-      int nxt = page(w.t0);
-      for (int t = w.t0; t < w.t1 && ok; ++t, ++j) {
-        const int blk = nxt;
-        nxt = page(t + 1);
-        const int np = __popc(__ballot_sync(0xffffffffu, blk >= 0));
-        const int y = blk << a.shift;
-        for (int ch = -1; ch < 4; ++ch) {
-          uint64_t *fb = ch < 0 ? &c.rope_full : &c.full[slot];
-          int good = 1;
-          if (lane == 0) {
-            if (ch < 0)
-              good = j < 1 || mbar_wait(&c.rope_empty, (j - 1) & 1, abort, a.status);
-            else
-              good = use == 0 || mbar_wait(&c.empty[slot], (use - 1) & 1, abort, a.status);
-            if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * bs * (ch < 0 ? 64 : 128)));
+      int nxt0 = page(w.t0, pg), nxt1 = page(w.t0, pg + 4);
+      for (int t = w.t0; t < w.t1; ++t, ++j) {
+        const int b0 = nxt0, b1 = nxt1;
+        nxt0 = page(t + 1, pg);
+        nxt1 = page(t + 1, pg + 4);
+        const int np = __popc(__ballot_sync(0xffffffffu, kd == 0 && b0 >= 0)) +
+                       __popc(__ballot_sync(0xffffffffu, kd == 0 && b1 >= 0));
+        const uint32_t item = 4 * j + kd, slot = item % NS, use = item / NS;
+        uint64_t *fb = kd == 4 ? &c.rope_full : &c.full[slot];
+        uint64_t *eb = kd == 4 ? &c.rope_empty : &c.empty[slot];
+        const uint32_t n_use = kd == 4 ? j : use;
+        uint8_t *dst = (kd == 4 ? sRope : sRing + slot * kPgSlot) + pg * bs * row_bytes;
+#pragma unroll 1
+        for (int g = 0; g < 3; ++g) {
+          const bool mine = kd >> 1 == g;
+          bool good = true;
+          if (arm && mine) {
+            good = n_use == 0 || mbar_wait(eb, (n_use - 1) & 1, abort, a.status);
+            if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * bs) * row_bytes);
           }
-          good = __shfl_sync(0xffffffffu, good, 0);
-          if (!good) {
+          if (!__all_sync(0xffffffffu, good)) {
             ok = false;
             break;
           }
-          if (blk >= 0) {
-            if (ch < 0)
-              tma_load_2d(sRope + lane * bs * 64, &tm_rope, CPMLA_DV, y, fb);
-            else
-              tma_load_2d(sRing + slot * kPgSlot + lane * bs * 128, &tm_lat, ch * 128, y, fb);
-          }
+          if (mine && b0 >= 0) tma_load_2d(dst, tm, kd * 128, b0 << a.shift, fb);
+          if (mine && b1 >= 0) tma_load_2d(dst + 4 * bs * row_bytes, tm, kd * 128, b1 << a.shift, fb);
           __syncwarp();
-          if (ch < 0) ++ropes;
-          if (ch >= 0 && ++slot == NS) {
-            slot = 0;
-            ++use;
-          }
+          items += g < 2 ? 2 : 0;
+          ropes += g == 2 ? 1 : 0;
         }
+        if (!ok) break;
       }
     }
     // giving up: the copies in flight have landed before the CTA exits
     if (!ok && lane == 0) {
-      const uint32_t n = use * NS + slot;
-      for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
+      for (uint32_t i = items > NS ? items - NS : 0; i < items; ++i)
         pg_drain(&c.full[i % NS], (i / NS) & 1, kPgDrainNs);
       if (ropes > 0) pg_drain(&c.rope_full, (ropes - 1) & 1, kPgDrainNs);
     }
