@@ -251,23 +251,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float *v) {
       "r"(__float_as_uint(v[15]))
       : "memory");
 }
-// 16 lanes x 64 columns: thread 4 r + c gets columns 8 i + 2 c, 8 i + 2 c + 1 (i
-// = 0..7) of lane r in v[4 i], v[4 i + 1] and of lane r + 8 in v[4 i + 2], v[4 i + 3].
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, float *v) {
-  uint32_t r[32];
+// 16 lanes, two spans of 16 columns: thread t gets lane t % 16, columns i (t < 16)
+// or kOff + i (t >= 16), i = 0..15.
+template <int kOff>
+__device__ __forceinline__ void tmem_ld_16x32bx2_x16(uint32_t taddr, float *v) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16], %17;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "n"(kOff));
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// The same layout stored, 8 columns.
+// 16 lanes x 8 columns stored: thread 4 r + c has columns 2 c, 2 c + 1 of lane r
+// in v0, v1 and of lane r + 8 in v2, v3.
 __device__ __forceinline__ void tmem_st_16x256b_x1(uint32_t taddr, uint32_t v0, uint32_t v1,
                                                    uint32_t v2, uint32_t v3) {
   asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v0),

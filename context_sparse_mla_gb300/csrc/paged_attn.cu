@@ -299,19 +299,19 @@ struct PgCfg {
   // cycles, most of them for the 4 KB of keys, which N = 48 reads once for three.
   static constexpr int kWide = R == 16 ? 3 : (R == 32 ? 2 : 1);
   static constexpr int kOW = R * kWide;  // columns of an O^T chunk
-  // R = 64: one P buffer (the parts wait in registers for the PV GEMM before) and
-  // two ring slots more: a tile holds its slots for about 2.5 tile times
-  static constexpr int kPB = R == 64 ? 1 : 2;
-  static constexpr int kFixed = kPgRope + kPB * kP + kPgRope;
+  // One P buffer (the parts wait in registers for the PV GEMM before) and more ring
+  // slots: a tile holds its slots for about 2.5 tile times
+  static constexpr int kRB = R == 64 ? 1 : 2;  // rope buffers
+  static constexpr int kFixed = kPgRope + kP + kRB * kPgRope;
   static constexpr int kSlots = R == 16 ? 12 : 11;
 };
 
 template <int R>
 struct PgCtrl {
   uint64_t full[PgCfg<R>::kSlots], empty[PgCfg<R>::kSlots];
-  uint64_t rope_full, rope_empty;
+  uint64_t rope_full[2], rope_empty[2];
   uint64_t s_full, s_free;
-  uint64_t p_full[2], p_free[2];
+  uint64_t p_full, p_free;
   uint64_t q_full[2];  // q in place, for even and odd pieces: a waiter may be a piece behind
   uint64_t q_free;
   uint64_t o_full, o_free;
@@ -319,7 +319,8 @@ struct PgCtrl {
   uint32_t tmem_base;
   int abort;
   float qf[2][R];      // a piece's scale of q row r, times softmax scale and log2 e
-  float stat_m[R], stat_l[R];
+  float stat_m[R], stat_l[2][R];
+  float red[2][R];  // a tile's row maxima, by half
   alignas(16) float alpha[R];
   // per softmax warp: a row's output factor and its place in the output
   alignas(16) float inv[kPgSmWarps][R / 2];
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                       const __grid_constant__ CUtensorMap tm_lat,
                       const __grid_constant__ CUtensorMap tm_rope) {
   using Cfg = PgCfg<R>;
-  constexpr int NS = Cfg::kSlots, PB = Cfg::kPB;
+  constexpr int NS = Cfg::kSlots, RB = Cfg::kRB;
   {
     const int4 s = a.start[blockIdx.x], e = a.start[blockIdx.x + 1];
     if (s.x == e.x && s.y == e.y && s.z == e.z) return;  // no tiles for this CTA
@@ -409,9 +410,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sQr = smem;                    // q's rope, [128 lanes x 64]
-  uint8_t *sP = sQr + kPgRope;            // P of three parts, one or two
-  uint8_t *sRope = sP + PB * Cfg::kP;     // [128 keys x 64]
-  uint8_t *sRing = sRope + kPgRope;
+  uint8_t *sP = sQr + kPgRope;            // P of three parts
+  uint8_t *sRope = sP + Cfg::kP;          // kRB of [128 keys x 64]
+  uint8_t *sRing = sRope + RB * kPgRope;
   PgCtrl<R> &c = *reinterpret_cast<PgCtrl<R> *>(sRing + NS * kPgSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -421,12 +422,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(&c.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&c.p_full[s], kPgSmWarps);
-      mbar_init(&c.p_free[s], 2);
+      mbar_init(&c.rope_full[s], 1);
+      mbar_init(&c.rope_empty[s], 1);
       mbar_init(&c.q_full[s], 4);
     }
-    mbar_init(&c.rope_full, 1);
-    mbar_init(&c.rope_empty, 1);
+    mbar_init(&c.p_full, kPgSmWarps);
+    mbar_init(&c.p_free, 2);
     mbar_init(&c.s_full, 1);
     mbar_init(&c.s_free, kPgSmWarps);
     mbar_init(&c.q_free, 1);
@@ -464,44 +465,57 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     while (ok && w.next(a)) {
       if (w.t1 <= w.t0) continue;
       for (int t = w.t0; t < w.t1; ++t, ++j) {
-        // lanes 0-3: the latent chunks, 4: the rope, 5: the scores' buffer, 6: q
-        uint64_t *bar = nullptr;
-        uint32_t par = j;
-        if (lane < 4) {
-          bar = &c.full[(4 * j + lane) % NS];
-          par = (4 * j + lane) / NS;
-        } else if (lane == 4) {
-          bar = &c.rope_full;
-        } else if (lane == 5 && j > 0) {
-          bar = &c.s_free;
-          par = j - 1;
-        } else if (lane == 6 && t == w.t0) {
-          bar = &c.q_full[piece & 1];
-          par = piece >> 1;
-        }
-        const bool good = !bar || mbar_wait(bar, par & 1, abort, a.status);
-        if (!__all_sync(0xffffffffu, good)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lane == 0) {
+        // two steps: chunks 0 and 1, then 2 and 3 and the rope
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const uint64_t db = dr + (((4 * j + ch) % NS * kPgSlot) >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f8_ts(tS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id,
-                        (ch | k) != 0 ? 1u : 0u);
+        for (int hf = 0; hf < 2; ++hf) {
+          // lanes 0, 1: the chunks, 2: the scores' buffer or the rope, 3: q
+          uint64_t *bar = nullptr;
+          uint32_t par = 0;
+          if (lane < 2) {
+            const uint32_t n = 4 * j + 2 * hf + lane;
+            bar = &c.full[n % NS];
+            par = n / NS;
+          } else if (lane == 2) {
+            if (hf == 1) {
+              bar = &c.rope_full[j % RB];
+              par = j / RB;
+            } else if (j > 0) {
+              bar = &c.s_free;
+              par = j - 1;
+            }
+          } else if (lane == 3 && hf == 0 && t == w.t0) {
+            bar = &c.q_full[piece & 1];
+            par = piece >> 1;
           }
+          const bool good = !bar || mbar_wait(bar, par & 1, abort, a.status);
+          if (!__all_sync(0xffffffffu, good)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma_f8_ss(tS, dqr + ((k * 32) >> 4), drr + ((k * 32) >> 4), id, 1u);
-          mma_commit(&c.s_full);
-          mma_commit(&c.rope_empty);
-          if (t + 1 == w.t1) mma_commit(&c.q_free);
+            for (int i = 0; i < 2; ++i) {
+              const int ch = 2 * hf + i;
+              const uint64_t db = dr + (((4 * j + ch) % NS * kPgSlot) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f8_ts(tS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id,
+                          (ch | k) != 0 ? 1u : 0u);
+            }
+            if (hf == 1) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma_f8_ss(tS, dqr + ((k * 32) >> 4), drr + ((j % RB * kPgRope + k * 32) >> 4), id,
+                          1u);
+              mma_commit(&c.s_full);
+              mma_commit(&c.rope_empty[j % RB]);
+              if (t + 1 == w.t1) mma_commit(&c.q_free);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
       }
       ++piece;
     }
@@ -532,13 +546,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           break;
         }
         for (int t = w.t0; t < w.t1; ++t, ++j) {
-          const uint32_t b = j % PB;
-          if (!mbar_wait(&c.p_full[b], (j / PB) & 1, abort, a.status)) {
+          if (!mbar_wait(&c.p_full, j & 1, abort, a.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t db = dp + ((b * Cfg::kP) >> 4);
 #pragma unroll 1
           for (int ch = me; ch < 4; ch += 2) {
             const uint32_t slot = (4 * j + ch) % NS;
@@ -549,13 +561,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
               for (uint32_t y = 0; y < kPgParts; y += W) {
                 mma_f8_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4),
-                          db + ((y * Cfg::kPart + k * 32) >> 4), y + W <= kPgParts ? id : id_rest,
+                          dp + ((y * Cfg::kPart + k * 32) >> 4), y + W <= kPgParts ? id : id_rest,
                           acc);
                 acc = 1;
               }
             mma_commit(&c.empty[slot]);
           }
-          mma_commit(&c.p_free[b]);
+          mma_commit(&c.p_free);
         }
         if (ok) mma_commit(&c.o_full);
         ++piece;
@@ -595,10 +607,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int np = __popc(__ballot_sync(0xffffffffu, kd == 0 && b0 >= 0)) +
                        __popc(__ballot_sync(0xffffffffu, kd == 0 && b1 >= 0));
         const uint32_t item = 4 * j + kd, slot = item % NS, use = item / NS;
-        uint64_t *fb = kd == 4 ? &c.rope_full : &c.full[slot];
-        uint64_t *eb = kd == 4 ? &c.rope_empty : &c.empty[slot];
-        const uint32_t n_use = kd == 4 ? j : use;
-        uint8_t *dst = (kd == 4 ? sRope : sRing + slot * kPgSlot) + pg * bs * row_bytes;
+        uint64_t *fb = kd == 4 ? &c.rope_full[j % RB] : &c.full[slot];
+        uint64_t *eb = kd == 4 ? &c.rope_empty[j % RB] : &c.empty[slot];
+        const uint32_t n_use = kd == 4 ? j / RB : use;
+        uint8_t *dst =
+            (kd == 4 ? sRope + j % RB * kPgRope : sRing + slot * kPgSlot) + pg * bs * row_bytes;
 #pragma unroll 1
         for (int g = 0; g < 3; ++g) {
           const bool mine = kd >> 1 == g;
@@ -624,19 +637,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     if (!ok && lane == 0) {
       for (uint32_t i = items > NS ? items - NS : 0; i < items; ++i)
         pg_drain(&c.full[i % NS], (i / NS) & 1, kPgDrainNs);
-      if (ropes > 0) pg_drain(&c.rope_full, (ropes - 1) & 1, kPgDrainNs);
+      for (uint32_t i = ropes > RB ? ropes - RB : 0; i < ropes; ++i)
+        pg_drain(&c.rope_full[i % RB], (i / RB) & 1, kPgDrainNs);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + kPgSmWarps) {
     // ------------------------------------------------------ softmax
-    // Of each 16 lanes of the scores the first 8 are the h parts of 8 q rows, the
-    // last 8 their l parts; a 16-lane load gives thread 4 r + c both parts of
-    // row r for keys 8 i + 2 c, 8 i + 2 c + 1 (i = 0..15), so a row belongs to four
-    // threads and its statistics need no other warp.  A warp that gives up
-    // goes on through the loop without waiting or writing, so that the barriers
-    // stay matched.
-    const int q4 = warp & 3, half = (warp - 4) >> 2, c4 = lane & 3;
-    const int r = q4 * 16 + half * 8 + (lane >> 2);
+    // Of a warp's 32 lanes of the scores the first 16 are the h parts of 16 q rows,
+    // the last 16 their l parts; threads r and r + 16 load both parts of row r,
+    // for 32 keys side by side each (a warpgroup half: keys 64 (lane / 16) + 32
+    // half ..).  So the rest of a row is one shuffle and the other half away, and a
+    // thread writes 32 bytes of each part of P.  A warp that gives up goes on
+    // through the loop without waiting or writing, so that the barriers stay
+    // matched.
+    const int q4 = warp & 3, half = (warp - 4) >> 2;
+    const int r = q4 * 16 + (lane & 15), kb = (lane >> 4) * 64 + half * 32;
+    const bool lead = half == 0 && lane < 16;  // speaks for its row
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     constexpr int kBar = 1, kBarN = 32 * kPgSmWarps;
     const bool live = q4 * 16 < R;  // the warp has rows
@@ -675,7 +691,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       for (int x = w.t0; x < w.t1; ++x, ++j) {
         const int e_nxt = exp_of_block(b_nxt);
         b_nxt = block_at(x + 2);
-        const uint32_t pb = j % PB;
         const int p0 = (w.m.t_lo + x) * 128;
         const bool open = p0 >= w.m.lo_max && p0 + 127 <= w.m.hi_min &&
                           __all_sync(0xffffffffu, e_cur >= 0);
@@ -689,26 +704,25 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         if (live && ok) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            float v[32];
-            tmem_ld_16x256b_x8(tS + lane_off + ((uint32_t)(half * 16) << 16) + g * 64, v);
+            float v[16];
+            const uint32_t col = tS + lane_off + half * 32 + g * 16;
+            tmem_ld_16x32bx2_x16<64>(col, s + 16 * g);
+            tmem_ld_16x32bx2_x16<64>(col + (16u << 16), v);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              s[g * 16 + 2 * i] = fmaf(v[4 * i + 2], 0.0625f, v[4 * i]);
-              s[g * 16 + 2 * i + 1] = fmaf(v[4 * i + 3], 0.0625f, v[4 * i + 1]);
-            }
+            for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(v[i], 0.0625f, s[16 * g + i]);
           }
         }
         tc_fence_before();
         if (ok) warp_arrive(&c.s_free, lane);
-        float um = -INFINITY;
+        float um = -INFINITY, kd[2];  // kd: 2^-e of the thread's two key groups
         if (live && ok) {
           if (!open) {
             // NaN codes in a key that not every row may see: weight zero times
             // NaN would reach the others, so the key's values become zero (a
             // row that does see it has a NaN weight).  A NaN code makes the
-            // scores of every row NaN, so any row's four threads know the keys;
-            // the warps share them out.
+            // scores of every row NaN, so any row's threads know the keys; the
+            // warps of a half share them out.
             uint32_t nan = 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) nan |= (uint32_t)(s[i] != s[i]) << i;
@@ -717,9 +731,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               // the copies are seen by this thread too (they landed long ago)
               (void)mbar_wait(&c.full[n % NS], (n / NS) & 1, abort, a.status);
               __syncwarp();
-              for (int k = q4 * 2 + half; k < 128; k += R / 8) {
-                const uint32_t nk = __shfl_sync(0xffffffffu, nan, (k >> 1) & 3);
-                if (((nk >> ((k >> 3) * 2 + (k & 1))) & 1) == 0) continue;
+              for (int i = q4; i < 64; i += R / 16) {
+                const uint32_t nk = __shfl_sync(0xffffffffu, nan, (i >> 5) * 16);
+                if (((nk >> (i & 31)) & 1) == 0) continue;
+                const int k = (i >> 5) * 64 + half * 32 + (i & 31);
                 uint4 *kr = reinterpret_cast<uint4 *>(sRing + (n % NS) * kPgSlot + k * 128 +
                                                       (lane & 7) * 16);
                 const uint4 v = *kr;
@@ -734,24 +749,30 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           // u = t + e
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float f = qf * __shfl_sync(0xffffffffu, kf, g);
-            const float k0 = __shfl_sync(0xffffffffu, ku, g);
+          for (int g = 0; g < 2; ++g) {
+            const float k2 = __shfl_sync(0xffffffffu, kf, (kb >> 4) + g);
+            const float k0 = __shfl_sync(0xffffffffu, ku, (kb >> 4) + g);
+            const float f = qf * k2;
+            // 2^-e: the exponent field mirrored about that of 1
+            kd[g] = __uint_as_float((254u << 23) - __float_as_uint(k2));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[4 * g + i] = fmaf(s[4 * g + i], f, k0);
+            for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(s[16 * g + i], f, k0);
           }
           if (!open) {
 #pragma unroll
             for (int n = 0; n < 32; ++n) {
-              const int p = p0 + 8 * (n >> 1) + 2 * c4 + (n & 1);
-              if (((there >> (n >> 2)) & 1) == 0 || p < lo || p > hi) s[n] = -INFINITY;
+              const int p = p0 + kb + n;
+              if (((there >> ((kb >> 4) + (n >> 4))) & 1) == 0 || p < lo || p > hi)
+                s[n] = -INFINITY;
             }
           }
 #pragma unroll
           for (int n = 0; n < 32; ++n) um = fmaxf(um, s[n]);
-          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
-          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
+          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 16));
+          if (lane < 16) c.red[half][r] = um;
         }
+        named_bar_sync(kBar, kBarN);
+        if (live) um = fmaxf(um, c.red[half ^ 1][r]);
         // the reference follows the tile's maximum when it leaves the window
         float m_new = m_ref;
         if (mine && um > -INFINITY) {
@@ -767,11 +788,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           const float al = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
           l = l == 0.f ? 0.f : l * al;
           if (x > w.t0) {
-            if (live && c4 == 0) c.alpha[r] = al;
+            if (live && lead) c.alpha[r] = al;
             named_bar_sync(kBar, kBarN);
             // the PV GEMM of the tile before is done with O^T
-            if (ok) ok = warp_wait(&c.p_free[(j - 1) % PB], ((j - 1) / PB) & 1, lane, abort,
-                                   a.status);
+            if (ok) ok = warp_wait(&c.p_free, (j - 1) & 1, lane, abort, a.status);
             tc_fence_after();
             if (ok) {
 #pragma unroll 1
@@ -796,15 +816,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         uint32_t part[kPgParts][8];
         if (live && ok) {
           const float mm = m_ref == -INFINITY ? 0.f : m_ref;
+          float sum[2] = {0.f, 0.f};
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
             float pv[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) pv[y] = fast_exp2(s[4 * g + y] - mm);
-            // 2^-e: the exponent field mirrored about that of 1
-            const float kd = __uint_as_float(
-                (254u << 23) - __float_as_uint(__shfl_sync(0xffffffffu, kf, g)));
-            l = fmaf((pv[0] + pv[1]) + (pv[2] + pv[3]), kd, l);
+            sum[g >> 2] += (pv[0] + pv[1]) + (pv[2] + pv[3]);
             uint32_t a0 = pack_f16x2(pv[0], pv[1]), a1 = pack_f16x2(pv[2], pv[3]);
 #pragma unroll
             for (int y = 0; y < kPgParts; ++y) {
@@ -819,34 +837,32 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               }
             }
           }
+          l = fmaf(sum[0], kd[0], fmaf(sum[1], kd[1], l));
         }
-        // this P buffer's last PV GEMM is done
-        if (ok && j >= PB)
-          ok = warp_wait(&c.p_free[pb], (j / PB - 1) & 1, lane, abort, a.status);
+        // the PV GEMM of the tile before is done with P
+        if (ok && j > 0) ok = warp_wait(&c.p_free, (j - 1) & 1, lane, abort, a.status);
         if (live && ok) {
-          uint8_t *pr = sP + pb * Cfg::kP + r * 128 + 2 * c4;
+          uint8_t *pr = sP + r * 128;
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            uint8_t *d = pr + ((g ^ (r & 7)) << 4);
+          for (int y = 0; y < kPgParts; ++y)
 #pragma unroll
-            for (int y = 0; y < kPgParts; ++y) {
-              *reinterpret_cast<uint16_t *>(d + y * Cfg::kPart) = (uint16_t)part[y][g];
-              *reinterpret_cast<uint16_t *>(d + y * Cfg::kPart + 8) = (uint16_t)(part[y][g] >> 16);
-            }
-          }
+            for (int g = 0; g < 2; ++g)
+              *reinterpret_cast<uint4 *>(pr + y * Cfg::kPart +
+                                         ((((kb >> 4) + g) ^ (r & 7)) << 4)) =
+                  make_uint4(part[y][4 * g], part[y][4 * g + 1], part[y][4 * g + 2],
+                             part[y][4 * g + 3]);
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        if (ok) warp_arrive(&c.p_full[pb], lane);
+        if (ok) warp_arrive(&c.p_full, lane);
         e_cur = e_nxt;
       }
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
       // ---------------------------------------------- this piece's O and LSE
       // A warp has a quarter of the channels (its TMEM lanes) and half of the rows.
-      if (live && c4 == 0) {
+      if (live && lane < 16) {
         c.stat_m[r] = m_ref;
-        c.stat_l[r] = l;
+        c.stat_l[half][r] = l;
       }
       named_bar_sync(kBar, kBarN);
       if (ok && some) ok = warp_wait(&c.o_full, piece & 1, lane, abort, a.status);
@@ -857,7 +873,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const bool whole = w.whole();
         if (lane < RH) {
           const int rr = half * RH + lane;
-          const float m = c.stat_m[rr], sl = c.stat_l[rr];
+          const float m = c.stat_m[rr], sl = c.stat_l[0][rr] + c.stat_l[1][rr];
           const bool empty = m == -INFINITY && sl == 0.f;  // l may be NaN
           const float l2 = empty ? -INFINITY : m + log2f(sl);
           float f = empty ? 0.f : 1.f / sl;
@@ -949,11 +965,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const int q4 = warp & 3;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     bool ok = true;
-    // q of piece k.  TMEM lane 16 x + 8 part + y of this warp's 32 is part h or
-    // l of row 16 q4 + 8 x + y: thread 4 y + c reads 8 channels of rows y (x = 0,
-    // 1), 32 channels a step with its quad, and its 16-lane store puts both
-    // parts where they belong.  The last two steps, the rope, go to shared
-    // memory.  (The loops are kept short: see the MMA issuers.)
+    // q of piece k.  TMEM lanes 0-15 of this warp's 32 are the h parts of rows 16
+    // q4 .., lanes 16-31 the l parts: thread 4 y + c reads 8 channels of rows y and y
+    // + 8, 32 channels a step with its quad, and two 16-lane stores put the parts
+    // where they belong.  The last two steps, the rope, go to shared memory.
+    // (The loops are kept short: see the MMA issuers.)
     auto load_q = [&](const PgWalk &v, uint32_t k) {
       const int r_valid = v.m.count * a.hc, y8 = lane >> 2, c4 = lane & 3;
       const uint4 *src[2];
@@ -1021,13 +1037,15 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         for (int n = 0; n < 16; n += 4) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            uint2 p[2][2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint2 p0 = split_q4(w[i][x].x, w[i][x].y, down[x]);
-              const uint2 p1 = split_q4(w[i][x].z, w[i][x].w, down[x]);
-              tmem_st_16x256b_x1(tmem + lane_off + ((uint32_t)(16 * x) << 16) + (n + i) * 8, p0.x,
-                                 p1.x, p0.y, p1.y);
+              p[x][0] = split_q4(w[i][x].x, w[i][x].y, down[x]);
+              p[x][1] = split_q4(w[i][x].z, w[i][x].w, down[x]);
             }
+            const uint32_t at = tmem + lane_off + (n + i) * 8;
+            tmem_st_16x256b_x1(at, p[0][0].x, p[0][1].x, p[1][0].x, p[1][1].x);
+            tmem_st_16x256b_x1(at + (16u << 16), p[0][0].y, p[0][1].y, p[1][0].y, p[1][1].y);
             fetch(min(n + i + 4, 17), w[i]);
           }
         }
@@ -1037,10 +1055,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           for (int x = 0; x < 2; ++x) {
             const uint2 p0 = split_q4(w[i][x].x, w[i][x].y, down[x]);
             const uint2 p1 = split_q4(w[i][x].z, w[i][x].w, down[x]);
-            const int ln = q4 * 32 + 16 * x + y8, ck = i * 2 + (c4 >> 1);
+            const int ln = q4 * 32 + 8 * x + y8, ck = i * 2 + (c4 >> 1);
             uint8_t *d = sQr + ln * 64 + ((ck ^ ((ln >> 1) & 3)) << 4) + (c4 & 1) * 8;
             *reinterpret_cast<uint2 *>(d) = make_uint2(p0.x, p1.x);
-            *reinterpret_cast<uint2 *>(d + 512) = make_uint2(p0.y, p1.y);  // lane + 8
+            *reinterpret_cast<uint2 *>(d + 1024) = make_uint2(p0.y, p1.y);  // lane + 16
           }
         tmem_st_wait();
         fence_proxy_async_smem();
