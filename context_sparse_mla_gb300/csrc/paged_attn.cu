@@ -49,8 +49,9 @@ namespace cpmla {
 namespace {
 
 constexpr int kPgMaxCtas = 160;   // at most one CTA per SM
-constexpr int kPgUnitTail = 3;    // a group's fixed cost, in tiles (plan)
-constexpr int kPgMinUnits = 4;    // tile units worth a CTA of its own
+constexpr int kPgTileLog = 6;     // 64 keys a tile
+constexpr int kPgUnitTail = 6;    // a group's fixed cost, in tiles (plan)
+constexpr int kPgMinUnits = 8;    // tile units worth a CTA of its own
 constexpr int kPgPlanThreads = 1024;
 
 struct PagedArgs {
@@ -81,7 +82,7 @@ struct PagedArgs {
 
 // Entries first .. first + count - 1: one request's tokens.
 struct PgGroup {
-  int first, count, req, t_lo;         // t_lo: first 128-key tile
+  int first, count, req, t_lo;         // t_lo: first tile
   int n_tiles, lo_min, hi_max, lo_max; // bounds over the rows that see a key
   int hi_min, pad;
   long long u0;                        // tile units before this group
@@ -160,8 +161,8 @@ __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedA
         ++m.count;
       } while ((tid + m.count) % a.g != 0 && s_b[tid + m.count] == e.b);
       if (m.hi_max >= 0) {
-        m.t_lo = m.lo_min >> 7;
-        m.n_tiles = (m.hi_max >> 7) - m.t_lo + 1;
+        m.t_lo = m.lo_min >> kPgTileLog;
+        m.n_tiles = (m.hi_max >> kPgTileLog) - m.t_lo + 1;
       }
     }
     const long long units = start ? (long long)a.n_hg * (m.n_tiles + kPgUnitTail) : 0;
@@ -284,47 +285,49 @@ struct PgWalk {
 
 // ------------------------------------------------------------- the attention
 constexpr int kPgThreads = 512;     // control, two softmax and one q warpgroup
-constexpr int kPgSmWarps = 8;
+constexpr int kPgTile = 1 << kPgTileLog;
 constexpr int kPgParts = 3;         // E5M2 parts of a weight
-constexpr int kPgSlot = 128 * 128;  // ring slot: [128 keys x 128 channels]
-constexpr int kPgRope = 128 * 64;   // [128 keys x 64], and q's [128 lanes x 64]
+constexpr int kPgSlot = kPgTile * 128;  // ring slot: [64 keys x 128 channels]
+constexpr int kPgRope = kPgTile * 64;   // [64 keys x 64]
+constexpr int kPgQRope = 128 * 64;      // q's rope: [128 lanes x 64]
 constexpr uint32_t kPgTmemCols = 512;
 
 template <int R>
 struct PgCfg {
-  static constexpr int kPart = R * 128;  // one part of P: [R rows x 128 keys]
+  static constexpr int kPart = R * kPgTile;  // one part of P: [R rows x 64 keys]
   static constexpr int kP = kPgParts * kPart;
   // Parts of P side by side in one PV MMA, each with accumulators of its own (TMEM
   // holds 4 R kWide + 256 columns): an MMA of N = 16, 32 or 64 takes 40, 40 or 48
   // cycles, most of them for the 4 KB of keys, which N = 48 reads once for three.
   static constexpr int kWide = R == 16 ? 3 : (R == 32 ? 2 : 1);
   static constexpr int kOW = R * kWide;  // columns of an O^T chunk
-  // One P buffer (the parts wait in registers for the PV GEMM before) and more ring
-  // slots: a tile holds its slots for about 2.5 tile times
-  static constexpr int kRB = R == 64 ? 1 : 2;  // rope buffers
-  static constexpr int kFixed = kPgRope + kP + kRB * kPgRope;
-  static constexpr int kSlots = R == 16 ? 12 : 11;
+  static constexpr int kRB = 4;          // rope buffers
+  static constexpr int kFixed = kPgQRope + 2 * kP + kRB * kPgRope;
+  static constexpr int kSlots = R == 16 ? 24 : (R == 32 ? 23 : 21);  // four a tile
 };
 
 template <int R>
 struct PgCtrl {
   uint64_t full[PgCfg<R>::kSlots], empty[PgCfg<R>::kSlots];
-  uint64_t rope_full[2], rope_empty[2];
-  uint64_t s_full, s_free;
-  uint64_t p_full, p_free;
-  uint64_t q_full[2];  // q in place, for even and odd pieces: a waiter may be a piece behind
-  uint64_t q_free;
-  uint64_t o_full, o_free;
+  uint64_t rope_full[PgCfg<R>::kRB], rope_empty[PgCfg<R>::kRB];
+  // S and P have a buffer for each softmax warpgroup: even and odd tiles
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[2], p_free[2];
+  uint64_t ref[4];     // row quarter's references of a tile are decided
+  // for even and odd pieces, as a waiter may be a piece behind: q is in place; the
+  // softmax is done with a piece, its output written
+  uint64_t q_full[2], o_free[2];
+  uint64_t q_free, o_full;
   uint64_t drain[3];
   uint32_t tmem_base;
   int abort;
   float qf[2][R];      // a piece's scale of q row r, times softmax scale and log2 e
-  float stat_m[R], stat_l[2][R];
-  float red[2][R];  // a tile's row maxima, by half
-  alignas(16) float alpha[R];
+  float m_ref[R], m_hi[R];
+  float stat_l[2][R];
+  alignas(16) float alpha[2][R];
   // per softmax warp: a row's output factor and its place in the output
-  alignas(16) float inv[kPgSmWarps][R / 2];
-  uint8_t *optr[kPgSmWarps][R / 2];
+  alignas(16) float inv[8][R / 2];
+  uint8_t *optr[8][R / 2];
 };
 template <int R>
 constexpr int pg_smem() {
@@ -410,8 +413,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sQr = smem;                    // q's rope, [128 lanes x 64]
-  uint8_t *sP = sQr + kPgRope;            // P of three parts
-  uint8_t *sRope = sP + Cfg::kP;          // kRB of [128 keys x 64]
+  uint8_t *sP = sQr + kPgQRope;           // two P of three parts
+  uint8_t *sRope = sP + 2 * Cfg::kP;      // kRB of [64 keys x 64]
   uint8_t *sRing = sRope + RB * kPgRope;
   PgCtrl<R> &c = *reinterpret_cast<PgCtrl<R> *>(sRing + NS * kPgSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -421,18 +424,21 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < RB; ++s) {
       mbar_init(&c.rope_full[s], 1);
       mbar_init(&c.rope_empty[s], 1);
-      mbar_init(&c.q_full[s], 4);
     }
-    mbar_init(&c.p_full, kPgSmWarps);
-    mbar_init(&c.p_free, 2);
-    mbar_init(&c.s_full, 1);
-    mbar_init(&c.s_free, kPgSmWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&c.s_full[s], 1);
+      mbar_init(&c.s_free[s], 4);
+      mbar_init(&c.p_full[s], 4);
+      mbar_init(&c.p_free[s], 2);
+      mbar_init(&c.q_full[s], 4);
+      mbar_init(&c.o_free[s], 8);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(&c.ref[s], 1);
     mbar_init(&c.q_free, 1);
     mbar_init(&c.o_full, 2);
-    mbar_init(&c.o_free, kPgSmWarps);
     for (int s = 0; s < 3; ++s) mbar_init(&c.drain[s], 1);
     c.abort = 0;
     fence_mbar_init();
@@ -446,8 +452,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem_base;
-  // columns: q [0, 128), S [128, 256), O^T chunk ch at tO + kOW ch
-  const uint32_t tS = tmem + 128, tO = tS + 128;
+  // columns: q [0, 128), S buffer b at tS + 64 b, O^T chunk ch at tO + kOW ch
+  const uint32_t tS = tmem + 128, tO = tS + 2 * kPgTile;
   volatile int *abort = &c.abort;
   PgWalk w(a, blockIdx.x);
 
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // The lanes wait side by side for what a tile needs (a wait that is over takes
     // 100-200 cycles all the same; one after another they took as long as the
     // MMAs), then lane 0 issues.
-    constexpr uint32_t id = idesc_e4m3(128, 128, 0, 0);
+    constexpr uint32_t id = idesc_e4m3(128, kPgTile, 0, 0);
     const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
     const uint64_t dr = smem_desc(smem_u32(sRing), 16, 1024, kSwz128);
     const uint64_t drr = smem_desc(smem_u32(sRope), 16, 512, kSwz64);
@@ -465,57 +471,46 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     while (ok && w.next(a)) {
       if (w.t1 <= w.t0) continue;
       for (int t = w.t0; t < w.t1; ++t, ++j) {
-        // two steps: chunks 0 and 1, then 2 and 3 and the rope
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          // lanes 0, 1: the chunks, 2: the scores' buffer or the rope, 3: q
-          uint64_t *bar = nullptr;
-          uint32_t par = 0;
-          if (lane < 2) {
-            const uint32_t n = 4 * j + 2 * hf + lane;
-            bar = &c.full[n % NS];
-            par = n / NS;
-          } else if (lane == 2) {
-            if (hf == 1) {
-              bar = &c.rope_full[j % RB];
-              par = j / RB;
-            } else if (j > 0) {
-              bar = &c.s_free;
-              par = j - 1;
-            }
-          } else if (lane == 3 && hf == 0 && t == w.t0) {
-            bar = &c.q_full[piece & 1];
-            par = piece >> 1;
-          }
-          const bool good = !bar || mbar_wait(bar, par & 1, abort, a.status);
-          if (!__all_sync(0xffffffffu, good)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int ch = 2 * hf + i;
-              const uint64_t db = dr + (((4 * j + ch) % NS * kPgSlot) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f8_ts(tS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id,
-                          (ch | k) != 0 ? 1u : 0u);
-            }
-            if (hf == 1) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_f8_ss(tS, dqr + ((k * 32) >> 4), drr + ((j % RB * kPgRope + k * 32) >> 4), id,
-                          1u);
-              mma_commit(&c.s_full);
-              mma_commit(&c.rope_empty[j % RB]);
-              if (t + 1 == w.t1) mma_commit(&c.q_free);
-            }
-          }
-          __syncwarp();
+        // lanes 0-3: the latent chunks, 4: the rope, 5: the scores' buffer, 6: q
+        uint64_t *bar = nullptr;
+        uint32_t par = 0;
+        if (lane < 4) {
+          bar = &c.full[(4 * j + lane) % NS];
+          par = (4 * j + lane) / NS;
+        } else if (lane == 4) {
+          bar = &c.rope_full[j % RB];
+          par = j / RB;
+        } else if (lane == 5 && j >= 2) {
+          bar = &c.s_free[j & 1];
+          par = (j >> 1) - 1;
+        } else if (lane == 6 && t == w.t0) {
+          bar = &c.q_full[piece & 1];
+          par = piece >> 1;
         }
-        if (!ok) break;
+        const bool good = !bar || mbar_wait(bar, par & 1, abort, a.status);
+        if (!__all_sync(0xffffffffu, good)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t dS = tS + (j & 1) * kPgTile;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            const uint64_t db = dr + (((4 * j + ch) % NS * kPgSlot) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f8_ts(dS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id,
+                        (ch | k) != 0 ? 1u : 0u);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            mma_f8_ss(dS, dqr + ((k * 32) >> 4), drr + ((j % RB * kPgRope + k * 32) >> 4), id, 1u);
+          mma_commit(&c.s_full[j & 1]);
+          mma_commit(&c.rope_empty[j % RB]);
+          if (t + 1 == w.t1) mma_commit(&c.q_free);
+        }
+        __syncwarp();
       }
       ++piece;
     }
@@ -535,18 +530,20 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       constexpr int W = Cfg::kWide, rest = kPgParts % W;  // parts a MMA, and in the last
       constexpr uint32_t id = idesc_e4m3_e5m2(128, R * W, 1, 0);
       constexpr uint32_t id_rest = idesc_e4m3_e5m2(128, R * (rest ? rest : W), 1, 0);
-      const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024, kSwz128);
+      const uint64_t dp = smem_desc(smem_u32(sP), 16, 512, kSwz64);
       const uint64_t dr = smem_desc(smem_u32(sRing), kPgSlot, 1024, kSwz128);
       bool ok = true;
       uint32_t j = 0, piece = 0;
       while (ok && w.next(a)) {
         if (w.t1 <= w.t0) continue;
-        if (piece > 0 && !mbar_wait(&c.o_free, (piece - 1) & 1, abort, a.status)) {
+        if (piece > 0 && !mbar_wait(&c.o_free[(piece - 1) & 1], ((piece - 1) >> 1) & 1, abort,
+                                     a.status)) {
           ok = false;
           break;
         }
         for (int t = w.t0; t < w.t1; ++t, ++j) {
-          if (!mbar_wait(&c.p_full, j & 1, abort, a.status)) {
+          const uint32_t b = j & 1;
+          if (!mbar_wait(&c.p_full[b], (j >> 1) & 1, abort, a.status)) {
             ok = false;
             break;
           }
@@ -557,17 +554,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             const uint64_t da = dr + ((slot * kPgSlot) >> 4);
             uint32_t acc = t > w.t0 ? 1u : 0u;
 #pragma unroll 1
-            for (uint32_t k = 0; k < 4; ++k)
+            for (uint32_t k = 0; k < kPgTile / 32; ++k)
 #pragma unroll
               for (uint32_t y = 0; y < kPgParts; y += W) {
                 mma_f8_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4),
-                          dp + ((y * Cfg::kPart + k * 32) >> 4), y + W <= kPgParts ? id : id_rest,
+                          dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4), y + W <= kPgParts ? id : id_rest,
                           acc);
                 acc = 1;
               }
             mma_commit(&c.empty[slot]);
           }
-          mma_commit(&c.p_free);
+          mma_commit(&c.p_free[b]);
         }
         if (ok) mma_commit(&c.o_full);
         ++piece;
@@ -580,81 +577,75 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------ loads
-    // Lane 5 p + x: chunk x (4: the rope) of page p of a tile, and of page p + 4
-    // where a tile has eight.  Chunks 0 and 1, then 2 and 3, then the rope: one
-    // instruction issues the boxes of all lanes concerned, about 80 cycles each
-    // (box after box, each behind its own wait, a tile's took 4200 cycles and
-    // bounded the kernel; all at once, the first slots would wait for the last).
-    const int bs = 1 << a.shift, ppt = 128 >> a.shift, pg = lane / 5, kd = lane - 5 * pg;
-    const bool act = pg < (ppt < 4 ? ppt : 4), arm = lane < 5;
+    // Lane 5 p + x: chunk x (4: the rope) of page p of a tile (a tile is half of a
+    // block of 128).  One instruction issues the boxes of all lanes, about 80
+    // cycles each; box after box, each behind its own wait, 128 keys took 4200
+    // cycles and bounded the kernel.
+    const int bs = 1 << a.shift, rows = bs < kPgTile ? bs : kPgTile, ppt = kPgTile / rows;
+    const int pg = lane / 5, kd = lane - 5 * pg;
+    const bool act = pg < ppt, arm = lane < 5;
     const uint32_t row_bytes = kd == 4 ? 64 : 128;
     const CUtensorMap *tm = kd == 4 ? &tm_rope : &tm_lat;
     bool ok = true;
-    uint32_t j = 0, items = 0, ropes = 0;
+    uint32_t j = 0;
     while (ok && w.next(a)) {
       const int32_t *row = a.table + (int64_t)w.m.req * a.stride;
-      auto page = [&](int t, int p) {
-        const int p0 = (w.m.t_lo + t) * 128 + p * bs;
-        if (!act || p >= ppt || t >= w.t1 || p0 > w.m.hi_max || p0 + bs <= w.m.lo_min) return -1;
+      // first row in the cache of this lane's page, or -1
+      auto page = [&](int t) {
+        const int p0 = ((w.m.t_lo + t) << kPgTileLog) + pg * rows;
+        if (!act || t >= w.t1 || p0 > w.m.hi_max || p0 + rows <= w.m.lo_min) return -1;
         const int blk = row[p0 >> a.shift];
-        return blk >= 0 && blk < a.n_blocks ? blk : -1;
+        return blk >= 0 && blk < a.n_blocks ? (blk << a.shift) + (p0 & (bs - 1)) : -1;
       };
-      int nxt0 = page(w.t0, pg), nxt1 = page(w.t0, pg + 4);
+      int nxt = page(w.t0);
       for (int t = w.t0; t < w.t1; ++t, ++j) {
-        const int b0 = nxt0, b1 = nxt1;
-        nxt0 = page(t + 1, pg);
-        nxt1 = page(t + 1, pg + 4);
-        const int np = __popc(__ballot_sync(0xffffffffu, kd == 0 && b0 >= 0)) +
-                       __popc(__ballot_sync(0xffffffffu, kd == 0 && b1 >= 0));
-        const uint32_t item = 4 * j + kd, slot = item % NS, use = item / NS;
+        const int y = nxt;
+        nxt = page(t + 1);
+        const int np = __popc(__ballot_sync(0xffffffffu, kd == 0 && y >= 0));
+        const uint32_t item = 4 * j + kd, slot = item % NS;
         uint64_t *fb = kd == 4 ? &c.rope_full[j % RB] : &c.full[slot];
         uint64_t *eb = kd == 4 ? &c.rope_empty[j % RB] : &c.empty[slot];
-        const uint32_t n_use = kd == 4 ? j / RB : use;
+        const uint32_t use = kd == 4 ? j / RB : item / NS;
         uint8_t *dst =
-            (kd == 4 ? sRope + j % RB * kPgRope : sRing + slot * kPgSlot) + pg * bs * row_bytes;
-#pragma unroll 1
-        for (int g = 0; g < 3; ++g) {
-          const bool mine = kd >> 1 == g;
-          bool good = true;
-          if (arm && mine) {
-            good = n_use == 0 || mbar_wait(eb, (n_use - 1) & 1, abort, a.status);
-            if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * bs) * row_bytes);
-          }
-          if (!__all_sync(0xffffffffu, good)) {
-            ok = false;
-            break;
-          }
-          if (mine && b0 >= 0) tma_load_2d(dst, tm, kd * 128, b0 << a.shift, fb);
-          if (mine && b1 >= 0) tma_load_2d(dst + 4 * bs * row_bytes, tm, kd * 128, b1 << a.shift, fb);
-          __syncwarp();
-          items += g < 2 ? 2 : 0;
-          ropes += g == 2 ? 1 : 0;
+            (kd == 4 ? sRope + j % RB * kPgRope : sRing + slot * kPgSlot) + pg * rows * row_bytes;
+        bool good = true;
+        if (arm) {
+          good = use == 0 || mbar_wait(eb, (use - 1) & 1, abort, a.status);
+          if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * rows) * row_bytes);
         }
-        if (!ok) break;
+        // (chunks armed beside one that gave up are waited for by nobody)
+        if (!__all_sync(0xffffffffu, good)) {
+          ok = false;
+          break;
+        }
+        if (y >= 0) tma_load_2d(dst, tm, kd * 128, y, fb);
+        __syncwarp();
       }
     }
     // giving up: the copies in flight have landed before the CTA exits
     if (!ok && lane == 0) {
-      for (uint32_t i = items > NS ? items - NS : 0; i < items; ++i)
+      for (uint32_t i = 4 * j > NS ? 4 * j - NS : 0; i < 4 * j; ++i)
         pg_drain(&c.full[i % NS], (i / NS) & 1, kPgDrainNs);
-      for (uint32_t i = ropes > RB ? ropes - RB : 0; i < ropes; ++i)
+      for (uint32_t i = j > RB ? j - RB : 0; i < j; ++i)
         pg_drain(&c.rope_full[i % RB], (i / RB) & 1, kPgDrainNs);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + kPgSmWarps) {
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------ softmax
+    // The two warpgroups take the tiles in turn, each with a score and a P buffer of
+    // its own, so that one's waits and shuffles run beside the other's arithmetic.
     // Of a warp's 32 lanes of the scores the first 16 are the h parts of 16 q rows,
     // the last 16 their l parts; threads r and r + 16 load both parts of row r,
-    // for 32 keys side by side each (a warpgroup half: keys 64 (lane / 16) + 32
-    // half ..).  So the rest of a row is one shuffle and the other half away, and a
-    // thread writes 32 bytes of each part of P.  A warp that gives up goes on
-    // through the loop without waiting or writing, so that the barriers stay
-    // matched.
-    const int q4 = warp & 3, half = (warp - 4) >> 2;
-    const int r = q4 * 16 + (lane & 15), kb = (lane >> 4) * 64 + half * 32;
-    const bool lead = half == 0 && lane < 16;  // speaks for its row
+    // for 32 keys side by side each, so the row's other half is one shuffle away.
+    // The references go from tile to tile in shared memory (warp q4 of one
+    // warpgroup to warp q4 of the other), each warpgroup's sums on the reference
+    // they last saw.  A warp that gives up goes on through the loop without
+    // waiting or writing, so that the barriers stay matched.
+    const int q4 = warp & 3, wg = (warp - 4) >> 2;
+    const int r = q4 * 16 + (lane & 15), kb = (lane >> 4) * 32;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    constexpr int kBar = 1, kBarN = 32 * kPgSmWarps;
+    const int bar_wg = 1 + wg;
+    constexpr int kBarAll = 3;
     const bool live = q4 * 16 < R;  // the warp has rows
     bool ok = true;
     uint32_t j = 0, piece = 0;
@@ -669,10 +660,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         hi = a.kv_hi ? min(a.kv_hi[i], a.pos[i]) : a.pos[i];
       }
       // group g of 16 keys of tile x (lane g and its copies): its block's stored
-      // exponent, or -1 where no row may look; the block of the next tile's
-      // group is fetched a tile ahead of its exponent
+      // exponent, or -1 where no row may look; the block of this warpgroup's next
+      // tile's group is fetched a tile ahead of its exponent
       auto block_at = [&](int x) {
-        const int p = (w.m.t_lo + x) * 128 + (lane & 7) * 16;
+        const int p = ((w.m.t_lo + x) << kPgTileLog) + (lane & 3) * 16;
         if (x >= w.t1 || p + 15 < w.m.lo_min || p > w.m.hi_max) return -1;
         const int blk = row[p >> a.shift];
         if (blk < 0 || blk >= a.n_blocks) {
@@ -682,39 +673,39 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         return blk;
       };
       auto exp_of_block = [&](int blk) { return blk >= 0 ? min((int)__ldg(a.exp + blk), 254) : -1; };
-      int e_cur = exp_of_block(block_at(w.t0));
-      int b_nxt = block_at(w.t0 + 1);
+      int x = w.t0 + ((j & 1) == (uint32_t)wg ? 0 : 1);  // this warpgroup's first tile
+      int e_cur = exp_of_block(block_at(x)), b_nxt = block_at(x + 2);
       if (ok && some)
         ok = warp_wait(&c.q_full[piece & 1], (piece >> 1) & 1, lane, abort, a.status);
       const float qf = ok && some && mine ? c.qf[piece & 1][r] : 0.f;
-      float m_ref = -INFINITY, m_hi = -INFINITY, l = 0.f;
-      for (int x = w.t0; x < w.t1; ++x, ++j) {
+      float m_own = -INFINITY, l = 0.f;  // the sum l is on reference m_own
+      for (uint32_t jj = j + (x - w.t0); x < w.t1; x += 2, jj += 2) {
         const int e_nxt = exp_of_block(b_nxt);
-        b_nxt = block_at(x + 2);
-        const int p0 = (w.m.t_lo + x) * 128;
-        const bool open = p0 >= w.m.lo_max && p0 + 127 <= w.m.hi_min &&
+        b_nxt = block_at(x + 4);
+        const int p0 = (w.m.t_lo + x) << kPgTileLog;
+        const bool open = p0 >= w.m.lo_max && p0 + kPgTile - 1 <= w.m.hi_min &&
                           __all_sync(0xffffffffu, e_cur >= 0);
         // 2^e and e of the key groups
         const float kf = e_cur >= 0 ? pg_pow2(e_cur) : 1.f;
         const float ku = (float)(e_cur - 127);
         const uint32_t there = __ballot_sync(0xffffffffu, e_cur >= 0);
-        if (ok) ok = warp_wait(&c.s_full, j & 1, lane, abort, a.status);
+        if (ok) ok = warp_wait(&c.s_full[wg], (jj >> 1) & 1, lane, abort, a.status);
         tc_fence_after();
         float s[32];
         if (live && ok) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float v[16];
-            const uint32_t col = tS + lane_off + half * 32 + g * 16;
-            tmem_ld_16x32bx2_x16<64>(col, s + 16 * g);
-            tmem_ld_16x32bx2_x16<64>(col + (16u << 16), v);
+            const uint32_t col = tS + wg * kPgTile + lane_off + g * 16;
+            tmem_ld_16x32bx2_x16<32>(col, s + 16 * g);
+            tmem_ld_16x32bx2_x16<32>(col + (16u << 16), v);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(v[i], 0.0625f, s[16 * g + i]);
           }
         }
         tc_fence_before();
-        if (ok) warp_arrive(&c.s_free, lane);
+        if (ok) warp_arrive(&c.s_free[wg], lane);
         float um = -INFINITY, kd[2];  // kd: 2^-e of the thread's two key groups
         if (live && ok) {
           if (!open) {
@@ -722,19 +713,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             // NaN would reach the others, so the key's values become zero (a
             // row that does see it has a NaN weight).  A NaN code makes the
             // scores of every row NaN, so any row's threads know the keys; the
-            // warps of a half share them out.
+            // warps share them out.
             uint32_t nan = 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) nan |= (uint32_t)(s[i] != s[i]) << i;
             if (__any_sync(0xffffffffu, nan != 0)) {
-              const uint32_t n = 4 * j + (lane >> 3);  // this lane's chunk of the tile
+              const uint32_t n = 4 * jj + (lane >> 3);  // this lane's chunk of the tile
               // the copies are seen by this thread too (they landed long ago)
               (void)mbar_wait(&c.full[n % NS], (n / NS) & 1, abort, a.status);
               __syncwarp();
-              for (int i = q4; i < 64; i += R / 16) {
-                const uint32_t nk = __shfl_sync(0xffffffffu, nan, (i >> 5) * 16);
-                if (((nk >> (i & 31)) & 1) == 0) continue;
-                const int k = (i >> 5) * 64 + half * 32 + (i & 31);
+              for (int k = q4; k < kPgTile; k += R / 16) {
+                const uint32_t nk = __shfl_sync(0xffffffffu, nan, (k >> 5) * 16);
+                if (((nk >> (k & 31)) & 1) == 0) continue;
                 uint4 *kr = reinterpret_cast<uint4 *>(sRing + (n % NS) * kPgSlot + k * 128 +
                                                       (lane & 7) * 16);
                 const uint4 v = *kr;
@@ -769,53 +759,63 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
           for (int n = 0; n < 32; ++n) um = fmaxf(um, s[n]);
           um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 16));
-          if (lane < 16) c.red[half][r] = um;
         }
-        named_bar_sync(kBar, kBarN);
-        if (live) um = fmaxf(um, c.red[half ^ 1][r]);
         // the reference follows the tile's maximum when it leaves the window
-        float m_new = m_ref;
+        float m_old = -INFINITY, m_hi = -INFINITY;
+        if (x > w.t0) {
+          if (ok) ok = warp_wait(&c.ref[q4], (jj - 1) & 1, lane, abort, a.status);
+          if (live) {
+            m_old = c.m_ref[r];
+            m_hi = c.m_hi[r];
+          }
+          __syncwarp();
+        }
+        float m_new = m_old;
         if (mine && um > -INFINITY) {
           m_hi = fmaxf(m_hi, um);
-          const float d = um - m_ref;  // +inf at a row's first key
+          const float d = um - m_old;  // +inf at a row's first key
           if (d > 15.75f)
             m_new = um - 10.f;
           else if (d < 4.f)
-            m_new = fminf(m_ref, fmaxf(um, m_hi - 60.f) - 10.f);
+            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) - 10.f);
         }
-        const bool moved = named_bar_or(kBar, kBarN, m_new != m_ref);
-        if (moved) {
-          const float al = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
-          l = l == 0.f ? 0.f : l * al;
-          if (x > w.t0) {
-            if (live && lead) c.alpha[r] = al;
-            named_bar_sync(kBar, kBarN);
-            // the PV GEMM of the tile before is done with O^T
-            if (ok) ok = warp_wait(&c.p_free, (j - 1) & 1, lane, abort, a.status);
-            tc_fence_after();
-            if (ok) {
+        if (live && lane < 16) {
+          c.m_ref[r] = m_new;
+          c.m_hi[r] = m_hi;
+        }
+        if (ok) warp_arrive(&c.ref[q4], lane);
+        if (m_new != m_own) {
+          l = l == 0.f ? 0.f : l * fast_exp2(m_own - m_new);
+          m_own = m_new;
+        }
+        if (x > w.t0 && named_bar_or(bar_wg, 128, m_new != m_old)) {
+          if (live && lane < 16)
+            c.alpha[wg][r] = m_old == -INFINITY ? 0.f : fast_exp2(m_old - m_new);
+          named_bar_sync(bar_wg, 128);
+          // the PV GEMM of the tile before is done with O^T
+          if (ok) ok = warp_wait(&c.p_free[wg ^ 1], ((jj - 1) >> 1) & 1, lane, abort, a.status);
+          tc_fence_after();
+          if (ok) {
 #pragma unroll 1
-              for (int col = half * 2 * Cfg::kOW; col < (half + 1) * 2 * Cfg::kOW; col += 16) {
-                float o[16];
-                tmem_ld16(tO + lane_off + col, o);
-                tmem_ld_wait();
+            for (int col = 0; col < 4 * Cfg::kOW; col += 16) {
+              float o[16];
+              tmem_ld16(tO + lane_off + col, o);
+              tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  o[i] = o[i] == 0.f ? 0.f : o[i] * c.alpha[(col % R) + i];
-                tmem_st16(tO + lane_off + col, o);
-              }
-              tmem_st_wait();
+              for (int i = 0; i < 16; ++i)
+                o[i] = o[i] == 0.f ? 0.f : o[i] * c.alpha[wg][(col % R) + i];
+              tmem_st16(tO + lane_off + col, o);
             }
-            named_bar_sync(kBar, kBarN);  // alpha is read
+            tmem_st_wait();
           }
-          m_ref = m_new;
+          named_bar_sync(bar_wg, 128);  // alpha is read
         }
         // p as fp16 bits, split by cutting: an E5M2 is the upper byte of an fp16, so
         // each part is the upper byte of what is left (nothing is negative); the
         // last part is rounded
         uint32_t part[kPgParts][8];
         if (live && ok) {
-          const float mm = m_ref == -INFINITY ? 0.f : m_ref;
+          const float mm = m_new == -INFINITY ? 0.f : m_new;
           float sum[2] = {0.f, 0.f};
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
@@ -839,32 +839,36 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           l = fmaf(sum[0], kd[0], fmaf(sum[1], kd[1], l));
         }
-        // the PV GEMM of the tile before is done with P
-        if (ok && j > 0) ok = warp_wait(&c.p_free, (j - 1) & 1, lane, abort, a.status);
+        // the PV GEMM of this buffer's last tile is done with it
+        if (ok && jj >= 2)
+          ok = warp_wait(&c.p_free[wg], ((jj >> 1) - 1) & 1, lane, abort, a.status);
         if (live && ok) {
-          uint8_t *pr = sP + r * 128;
+          uint8_t *pr = sP + wg * Cfg::kP + r * kPgTile;
 #pragma unroll
           for (int y = 0; y < kPgParts; ++y)
 #pragma unroll
             for (int g = 0; g < 2; ++g)
               *reinterpret_cast<uint4 *>(pr + y * Cfg::kPart +
-                                         ((((kb >> 4) + g) ^ (r & 7)) << 4)) =
+                                         ((((kb >> 4) + g) ^ ((r >> 1) & 3)) << 4)) =
                   make_uint4(part[y][4 * g], part[y][4 * g + 1], part[y][4 * g + 2],
                              part[y][4 * g + 3]);
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        if (ok) warp_arrive(&c.p_full, lane);
+        if (ok) warp_arrive(&c.p_full[wg], lane);
         e_cur = e_nxt;
       }
+      j += w.t1 - w.t0;
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       // ---------------------------------------------- this piece's O and LSE
       // A warp has a quarter of the channels (its TMEM lanes) and half of the rows.
+      named_bar_sync(kBarAll, 256);  // both have decided their last references
       if (live && lane < 16) {
-        c.stat_m[r] = m_ref;
-        c.stat_l[half][r] = l;
+        if (!some && wg == 0) c.m_ref[r] = -INFINITY;
+        const float m = some ? c.m_ref[r] : -INFINITY;
+        c.stat_l[wg][r] = l == 0.f ? 0.f : l * fast_exp2(m_own - m);
       }
-      named_bar_sync(kBar, kBarN);
+      named_bar_sync(kBarAll, 256);
       if (ok && some) ok = warp_wait(&c.o_full, piece & 1, lane, abort, a.status);
       tc_fence_after();
       if (ok) {
@@ -872,8 +876,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int sw = warp - 4, r_valid = w.m.count * a.hc, h0 = w.hg * a.hc;
         const bool whole = w.whole();
         if (lane < RH) {
-          const int rr = half * RH + lane;
-          const float m = c.stat_m[rr], sl = c.stat_l[0][rr] + c.stat_l[1][rr];
+          const int rr = wg * RH + lane;
+          const float m = c.m_ref[rr], sl = c.stat_l[0][rr] + c.stat_l[1][rr];
           const bool empty = m == -INFINITY && sl == 0.f;  // l may be NaN
           const float l2 = empty ? -INFINITY : m + log2f(sl);
           float f = empty ? 0.f : 1.f / sl;
@@ -899,7 +903,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int odd = lane & 1, t = q4 * 32 + lane;
         // RS rows (columns of O^T) of a channel chunk at a time
 #pragma unroll 1
-        for (int cb = 0; cb < RH && half * RH + cb < r_valid; cb += RS) {
+        for (int cb = 0; cb < RH && wg * RH + cb < r_valid; cb += RS) {
           float f[RS];
           uint8_t *p[RS / 2];  // rows cb + 2 y + odd
 #pragma unroll
@@ -913,7 +917,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               float w3[Cfg::kWide][RS];
 #pragma unroll
               for (int y = 0; y < Cfg::kWide; ++y) {
-                const uint32_t col = tO + lane_off + ch * Cfg::kOW + y * R + half * RH + cb;
+                const uint32_t col = tO + lane_off + ch * Cfg::kOW + y * R + wg * RH + cb;
                 if (RS == 16)
                   tmem_ld16(col, w3[y]);
                 else
@@ -955,12 +959,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       }
       tc_fence_before();
       if (some) {
-        if (ok) warp_arrive(&c.o_free, lane);
+        if (ok) warp_arrive(&c.o_free[piece & 1], lane);
         ++piece;
       }
-      named_bar_sync(kBar, kBarN);  // the statistics are read
+      named_bar_sync(kBarAll, 256);  // the statistics are read
     }
-  } else if (warp >= 4 + kPgSmWarps) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------ q into TMEM
     const int q4 = warp & 3;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
@@ -1024,9 +1028,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // a row with an infinite or NaN channel is NaN throughout
         up[x] = m >= 0x7F80u ? NAN : __int_as_float((127 + ae) << 23) * a.scale_log2;
       }
-      // the score GEMMs of the piece before are done with q (and so the softmax is
-      // past the start of that piece, and done with the scales of the one before)
-      if (k > 0) ok = warp_wait(&c.q_free, (k - 1) & 1, lane, abort, a.status);
+      // the softmax is done with the piece two before (its scales' place is used
+      // again, and it has seen that piece's q_full), the score GEMMs with q
+      if (k > 1) ok = warp_wait(&c.o_free[k & 1], ((k >> 1) - 1) & 1, lane, abort, a.status);
+      if (k > 0 && ok) ok = warp_wait(&c.q_free, (k - 1) & 1, lane, abort, a.status);
       if (!ok) return;
       tc_fence_after();
       if (q4 * 16 < R) {
@@ -1270,8 +1275,8 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
   a.groups = reinterpret_cast<PgGroup *>(ws + L.groups);
   a.lse_part = reinterpret_cast<float *>(ws + L.lse);
   a.o_part = reinterpret_cast<float *>(ws + L.o);
-  // the cache as [slots, 576] bytes in boxes of one block x 128 latent or the
-  // 64 rope channels, swizzled as the MMA reads them
+  // the cache as [slots, 576] bytes in boxes of one block (of at most a tile's rows)
+  // x 128 latent or the 64 rope channels, swizzled as the MMA reads them
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(CPMLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
   CUtensorMap tm[2];
@@ -1279,7 +1284,8 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
     memset(&tm[i], 0, sizeof tm[i]);
     cuuint64_t dims[2] = {CPMLA_DQK, (cuuint64_t)n_blocks * block_size};
     cuuint64_t strides[1] = {CPMLA_DQK};
-    cuuint32_t box[2] = {i == 0 ? 128u : 64u, (cuuint32_t)block_size};
+    cuuint32_t box[2] = {i == 0 ? 128u : 64u,
+                         (cuuint32_t)(block_size < kPgTile ? block_size : kPgTile)};
     cuuint32_t estr[2] = {1, 1};
     const CUresult cr =
         enc(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(cache), dims, strides, box,
