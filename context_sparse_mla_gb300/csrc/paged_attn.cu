@@ -287,9 +287,9 @@ struct PgWalk {
 constexpr int kPgThreads = 512;     // control, two softmax and one q warpgroup
 constexpr int kPgTile = 1 << kPgTileLog;
 constexpr int kPgParts = 3;         // E5M2 parts of a weight
-constexpr int kPgSlot = kPgTile * 128;  // ring slot: [64 keys x 128 channels]
+constexpr int kPgSlot = kPgTile * 128;  // a latent chunk: [64 keys x 128 channels]
 constexpr int kPgRope = kPgTile * 64;   // [64 keys x 64]
-constexpr int kPgQRope = 128 * 64;      // q's rope: [128 lanes x 64]
+constexpr int kPgTileBytes = 4 * kPgSlot + kPgRope;  // ring slot: a tile
 constexpr uint32_t kPgTmemCols = 512;
 
 template <int R>
@@ -301,15 +301,14 @@ struct PgCfg {
   // cycles, most of them for the 4 KB of keys, which N = 48 reads once for three.
   static constexpr int kWide = R == 16 ? 3 : (R == 32 ? 2 : 1);
   static constexpr int kOW = R * kWide;  // columns of an O^T chunk
-  static constexpr int kRB = 4;          // rope buffers
-  static constexpr int kFixed = kPgQRope + 2 * kP + kRB * kPgRope;
-  static constexpr int kSlots = R == 16 ? 24 : (R == 32 ? 23 : 21);  // four a tile
+  static constexpr int kQRope = 2 * R * 64;  // q's rope: [2R lanes x 64]
+  static constexpr int kFixed = kQRope + 2 * kP;
+  static constexpr int kSlots = R == 16 ? 6 : 5;  // tiles in the ring
 };
 
 template <int R>
 struct PgCtrl {
-  uint64_t full[PgCfg<R>::kSlots], empty[PgCfg<R>::kSlots];
-  uint64_t rope_full[PgCfg<R>::kRB], rope_empty[PgCfg<R>::kRB];
+  uint64_t full[PgCfg<R>::kSlots], empty[PgCfg<R>::kSlots];  // ring slots
   // S and P have a buffer for each softmax warpgroup: even and odd tiles
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2], p_free[2];
@@ -331,7 +330,7 @@ struct PgCtrl {
 };
 template <int R>
 constexpr int pg_smem() {
-  return 1024 + PgCfg<R>::kFixed + PgCfg<R>::kSlots * kPgSlot + (int)sizeof(PgCtrl<R>);
+  return 1024 + PgCfg<R>::kFixed + PgCfg<R>::kSlots * kPgTileBytes + (int)sizeof(PgCtrl<R>);
 }
 static_assert(pg_smem<64>() <= 232448 && pg_smem<32>() <= 232448 && pg_smem<16>() <= 232448,
               "shared memory budget");
@@ -405,28 +404,24 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                       const __grid_constant__ CUtensorMap tm_lat,
                       const __grid_constant__ CUtensorMap tm_rope) {
   using Cfg = PgCfg<R>;
-  constexpr int NS = Cfg::kSlots, RB = Cfg::kRB;
+  constexpr int NS = Cfg::kSlots;
   {
     const int4 s = a.start[blockIdx.x], e = a.start[blockIdx.x + 1];
     if (s.x == e.x && s.y == e.y && s.z == e.z) return;  // no tiles for this CTA
   }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sQr = smem;                    // q's rope, [128 lanes x 64]
-  uint8_t *sP = sQr + kPgQRope;           // two P of three parts
-  uint8_t *sRope = sP + 2 * Cfg::kP;      // kRB of [64 keys x 64]
-  uint8_t *sRing = sRope + RB * kPgRope;
-  PgCtrl<R> &c = *reinterpret_cast<PgCtrl<R> *>(sRing + NS * kPgSlot);
+  uint8_t *sQr = smem;                    // q's rope (the MMA reads 128 lanes; those behind
+                                          // 2R are whatever follows, and not used)
+  uint8_t *sP = sQr + Cfg::kQRope;        // two P of three parts
+  uint8_t *sRing = sP + 2 * Cfg::kP;      // tiles: four latent chunks, the rope
+  PgCtrl<R> &c = *reinterpret_cast<PgCtrl<R> *>(sRing + NS * kPgTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&c.full[s], 1);
-      mbar_init(&c.empty[s], 1);
-    }
-    for (int s = 0; s < RB; ++s) {
-      mbar_init(&c.rope_full[s], 1);
-      mbar_init(&c.rope_empty[s], 1);
+      mbar_init(&c.empty[s], 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.s_full[s], 1);
@@ -459,64 +454,47 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ score-GEMM issuer
-    // The lanes wait side by side for what a tile needs (a wait that is over takes
-    // 100-200 cycles all the same; one after another they took as long as the
-    // MMAs), then lane 0 issues.
-    constexpr uint32_t id = idesc_e4m3(128, kPgTile, 0, 0);
-    const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
-    const uint64_t dr = smem_desc(smem_u32(sRing), 16, 1024, kSwz128);
-    const uint64_t drr = smem_desc(smem_u32(sRope), 16, 512, kSwz64);
-    bool ok = true;
-    uint32_t j = 0, piece = 0;
-    while (ok && w.next(a)) {
-      if (w.t1 <= w.t0) continue;
-      for (int t = w.t0; t < w.t1; ++t, ++j) {
-        // lanes 0-3: the latent chunks, 4: the rope, 5: the scores' buffer, 6: q
-        uint64_t *bar = nullptr;
-        uint32_t par = 0;
-        if (lane < 4) {
-          bar = &c.full[(4 * j + lane) % NS];
-          par = (4 * j + lane) / NS;
-        } else if (lane == 4) {
-          bar = &c.rope_full[j % RB];
-          par = j / RB;
-        } else if (lane == 5 && j >= 2) {
-          bar = &c.s_free[j & 1];
-          par = (j >> 1) - 1;
-        } else if (lane == 6 && t == w.t0) {
-          bar = &c.q_full[piece & 1];
-          par = piece >> 1;
-        }
-        const bool good = !bar || mbar_wait(bar, par & 1, abort, a.status);
-        if (!__all_sync(0xffffffffu, good)) {
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_e4m3(128, kPgTile, 0, 0);
+      const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
+      const uint64_t dr = smem_desc(smem_u32(sRing), 16, 1024, kSwz128);
+      const uint64_t drr = smem_desc(smem_u32(sRing + 4 * kPgSlot), 16, 512, kSwz64);
+      bool ok = true;
+      uint32_t j = 0, piece = 0;
+      while (ok && w.next(a)) {
+        if (w.t1 <= w.t0) continue;
+        if (!mbar_wait(&c.q_full[piece & 1], (piece >> 1) & 1, abort, a.status)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t dS = tS + (j & 1) * kPgTile;
+        for (int t = w.t0; t < w.t1; ++t, ++j) {
+          const uint32_t slot = j % NS, dS = tS + (j & 1) * kPgTile;
+          if ((j >= 2 && !mbar_wait(&c.s_free[j & 1], ((j >> 1) - 1) & 1, abort, a.status)) ||
+              !mbar_wait(&c.full[slot], (j / NS) & 1, abort, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t db = dr + ((slot * kPgTileBytes) >> 4);
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const uint64_t db = dr + (((4 * j + ch) % NS * kPgSlot) >> 4);
+          for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8_ts(dS, tmem + ch * 32 + k * 8, db + ((k * 32) >> 4), id,
+              mma_f8_ts(dS, tmem + ch * 32 + k * 8, db + ((ch * kPgSlot + k * 32) >> 4), id,
                         (ch | k) != 0 ? 1u : 0u);
-          }
+          const uint64_t drb = drr + ((slot * kPgTileBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            mma_f8_ss(dS, dqr + ((k * 32) >> 4), drr + ((j % RB * kPgRope + k * 32) >> 4), id, 1u);
+            mma_f8_ss(dS, dqr + ((k * 32) >> 4), drb + ((k * 32) >> 4), id, 1u);
           mma_commit(&c.s_full[j & 1]);
-          mma_commit(&c.rope_empty[j % RB]);
-          if (t + 1 == w.t1) mma_commit(&c.q_free);
         }
-        __syncwarp();
+        if (ok) mma_commit(&c.q_free);
+        ++piece;
       }
-      ++piece;
-    }
-    if (!ok && lane == 0) {
-      mma_commit(&c.drain[0]);
-      pg_drain(&c.drain[0], 0, kWaitLimitNs);
+      if (!ok) {
+        mma_commit(&c.drain[0]);
+        pg_drain(&c.drain[0], 0, kWaitLimitNs);
+      }
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
@@ -550,8 +528,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           tc_fence_after();
 #pragma unroll 1
           for (int ch = me; ch < 4; ch += 2) {
-            const uint32_t slot = (4 * j + ch) % NS;
-            const uint64_t da = dr + ((slot * kPgSlot) >> 4);
+            const uint64_t da = dr + ((j % NS * kPgTileBytes + ch * kPgSlot) >> 4);
             uint32_t acc = t > w.t0 ? 1u : 0u;
 #pragma unroll 1
             for (uint32_t k = 0; k < kPgTile / 32; ++k)
@@ -562,8 +539,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                           acc);
                 acc = 1;
               }
-            mma_commit(&c.empty[slot]);
           }
+          mma_commit(&c.empty[j % NS]);
           mma_commit(&c.p_free[b]);
         }
         if (ok) mma_commit(&c.o_full);
@@ -583,8 +560,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // cycles and bounded the kernel.
     const int bs = 1 << a.shift, rows = bs < kPgTile ? bs : kPgTile, ppt = kPgTile / rows;
     const int pg = lane / 5, kd = lane - 5 * pg;
-    const bool act = pg < ppt, arm = lane < 5;
-    const uint32_t row_bytes = kd == 4 ? 64 : 128;
+    const bool act = pg < ppt;
     const CUtensorMap *tm = kd == 4 ? &tm_rope : &tm_lat;
     bool ok = true;
     uint32_t j = 0;
@@ -602,18 +578,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int y = nxt;
         nxt = page(t + 1);
         const int np = __popc(__ballot_sync(0xffffffffu, kd == 0 && y >= 0));
-        const uint32_t item = 4 * j + kd, slot = item % NS;
-        uint64_t *fb = kd == 4 ? &c.rope_full[j % RB] : &c.full[slot];
-        uint64_t *eb = kd == 4 ? &c.rope_empty[j % RB] : &c.empty[slot];
-        const uint32_t use = kd == 4 ? j / RB : item / NS;
-        uint8_t *dst =
-            (kd == 4 ? sRope + j % RB * kPgRope : sRing + slot * kPgSlot) + pg * rows * row_bytes;
+        const uint32_t slot = j % NS;
+        uint64_t *fb = &c.full[slot];
+        uint8_t *dst = sRing + slot * kPgTileBytes + kd * kPgSlot + pg * rows * (kd == 4 ? 64 : 128);
         bool good = true;
-        if (arm) {
-          good = use == 0 || mbar_wait(eb, (use - 1) & 1, abort, a.status);
-          if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * rows) * row_bytes);
+        if (lane == 0) {
+          good = j < NS || mbar_wait(&c.empty[slot], (j / NS - 1) & 1, abort, a.status);
+          if (good) mbar_arrive_expect_tx(fb, (uint32_t)(np * rows) * CPMLA_DQK);
         }
-        // (chunks armed beside one that gave up are waited for by nobody)
         if (!__all_sync(0xffffffffu, good)) {
           ok = false;
           break;
@@ -624,10 +596,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
     // giving up: the copies in flight have landed before the CTA exits
     if (!ok && lane == 0) {
-      for (uint32_t i = 4 * j > NS ? 4 * j - NS : 0; i < 4 * j; ++i)
+      for (uint32_t i = j > NS ? j - NS : 0; i < j; ++i)
         pg_drain(&c.full[i % NS], (i / NS) & 1, kPgDrainNs);
-      for (uint32_t i = j > RB ? j - RB : 0; i < j; ++i)
-        pg_drain(&c.rope_full[i % RB], (i / RB) & 1, kPgDrainNs);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
@@ -718,15 +688,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) nan |= (uint32_t)(s[i] != s[i]) << i;
             if (__any_sync(0xffffffffu, nan != 0)) {
-              const uint32_t n = 4 * jj + (lane >> 3);  // this lane's chunk of the tile
               // the copies are seen by this thread too (they landed long ago)
-              (void)mbar_wait(&c.full[n % NS], (n / NS) & 1, abort, a.status);
+              (void)mbar_wait(&c.full[jj % NS], (jj / NS) & 1, abort, a.status);
               __syncwarp();
               for (int k = q4; k < kPgTile; k += R / 16) {
                 const uint32_t nk = __shfl_sync(0xffffffffu, nan, (k >> 5) * 16);
                 if (((nk >> (k & 31)) & 1) == 0) continue;
-                uint4 *kr = reinterpret_cast<uint4 *>(sRing + (n % NS) * kPgSlot + k * 128 +
-                                                      (lane & 7) * 16);
+                uint4 *kr = reinterpret_cast<uint4 *>(
+                    sRing + jj % NS * kPgTileBytes + (lane >> 3) * kPgSlot + k * 128 + (lane & 7) * 16);
                 const uint4 v = *kr;
                 auto has = [](uint32_t u) {
                   const uint32_t z = ~u & 0x7F7F7F7Fu;  // a zero byte: a NaN code
