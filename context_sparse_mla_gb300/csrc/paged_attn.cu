@@ -13,13 +13,13 @@
 //   * p_j = 2^(u_j - m), as fp16, is the sum of three E5M2: 9 significant bits
 //     (a bf16 has 8) where p >= 2^-8, and at worst 2^-17 off below.  m follows
 //     each tile's maximum both ways: it moves when the tile's largest p leaves
-//     [2^4, 2^15.75], to make it 2^10, so weights keep their 9 bits down to
-//     2^-12 of a tile's own largest one at least, whatever the other tiles
-//     hold.  (A first token with almost all of the weight and next to no value
-//     is common; two E4M3 terms, which need a third fewer MMAs, reach 2^-9 and
-//     lose the tokens beside it.)  m stays within 2^60 of its highest value,
+//     [2^0, 2^15.75], to make it 2^8, so weights keep their 9 bits down to 2^-8 of
+//     a tile's own largest one at least (2^-16 where m was just set), whatever the
+//     other tiles hold.  (A first token with almost all of the weight and next to
+//     no value is common; two E4M3 terms, which need a third fewer MMAs, reach
+//     2^-9 and lose the tokens beside it.)  A move rescales O^T, a few thousand
+//     cycles, hence the wide window.  m stays within 2^60 of its highest value,
 //     beyond which a tile adds nothing.
-//
 // One CTA works on R = 64 rows (G tokens of one request x Hc heads) and 128
 // keys at a time, as the dense kernel does:
 //   S^T = C . [h | l]^T   M = 128 keys, N = 128, K = 576 (kind::f8f6f4), into
@@ -35,8 +35,8 @@
 // group that is cut leaves normalised fp32 parts in the workspace, at most two
 // for each SM, and a third launch joins them in a fixed order.
 //
-// Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (chunks 0, 2 and 1, 3),
-// 3 loads, 4-11 do the
+// Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (R < 64: 0 and 2, and 1), 3
+// loads, 4-11 do the
 // softmax and the output, 12-15 bring q in.  Every wait is
 // bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains its copies and
 // MMAs, frees TMEM and exits.
@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kPgMaxCtas = 160;   // at most one CTA per SM
 constexpr int kPgTileLog = 6;     // 64 keys a tile
-constexpr int kPgUnitTail = 6;    // a group's fixed cost, in tiles (plan)
+constexpr int kPgUnitTail = 12;   // a group's fixed cost, in tiles (plan)
 constexpr int kPgMinUnits = 8;    // tile units worth a CTA of its own
 constexpr int kPgPlanThreads = 1024;
 
@@ -301,6 +301,9 @@ struct PgCfg {
   // cycles, most of them for the 4 KB of keys, which N = 48 reads once for three.
   static constexpr int kWide = R == 16 ? 3 : (R == 32 ? 2 : 1);
   static constexpr int kOW = R * kWide;  // columns of an O^T chunk
+  // MMA issuers (warps 0-2): R = 64 has 24 PV MMAs a tile for two threads beside the
+  // 18 of the scores, fewer rows 8 or 16 for one, and the scores two
+  static constexpr int kPvW = R == 64 ? 2 : 1, kQkW = 3 - kPvW;
   static constexpr int kQRope = 2 * R * 64;  // q's rope: [2R lanes x 64]
   static constexpr int kFixed = kQRope + 2 * kP;
   static constexpr int kSlots = R == 16 ? 6 : 5;  // tiles in the ring
@@ -324,9 +327,9 @@ struct PgCtrl {
   float m_ref[R], m_hi[R];
   float stat_l[2][R];
   alignas(16) float alpha[2][R];
-  // per softmax warp: a row's output factor and its place in the output
+  // per softmax warp: a row's output factor and its row of the output (-1: none)
   alignas(16) float inv[8][R / 2];
-  uint8_t *optr[8][R / 2];
+  int64_t orow[8][R / 2];
 };
 template <int R>
 constexpr int pg_smem() {
@@ -385,19 +388,6 @@ __device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, float down) 
 __device__ __forceinline__ float pg_pow2(int stored) {
   return stored == 0 ? 5.877471754e-39f : __int_as_float(stored << 23);
 }
-// Predicated stores (no branch each): only where `p` is not NULL.
-__device__ __forceinline__ void st_global_if(const void *p, void *dst, uint32_t v) {
-  asm volatile("{\n .reg .pred q;\n setp.ne.u64 q, %0, 0;\n @q st.global.b32 [%1], %2;\n}\n" ::"l"(p),
-               "l"(dst), "r"(v)
-               : "memory");
-}
-__device__ __forceinline__ void st_global_if(const void *p, void *dst, float v0, float v1) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.u64 q, %0, 0;\n @q st.global.v2.f32 [%1], {%2, %3};\n}\n" ::"l"(p),
-      "l"(dst), "f"(v0), "f"(v1)
-      : "memory");
-}
-
 template <int R>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedArgs a,
@@ -421,19 +411,19 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&c.full[s], 1);
-      mbar_init(&c.empty[s], 2);
+      mbar_init(&c.empty[s], Cfg::kPvW);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.s_free[s], 4);
       mbar_init(&c.p_full[s], 4);
-      mbar_init(&c.p_free[s], 2);
+      mbar_init(&c.p_free[s], Cfg::kPvW);
       mbar_init(&c.q_full[s], 4);
       mbar_init(&c.o_free[s], 8);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&c.ref[s], 1);
-    mbar_init(&c.q_free, 1);
-    mbar_init(&c.o_full, 2);
+    mbar_init(&c.q_free, Cfg::kQkW);
+    mbar_init(&c.o_full, Cfg::kPvW);
     for (int s = 0; s < 3; ++s) mbar_init(&c.drain[s], 1);
     c.abort = 0;
     fence_mbar_init();
@@ -452,8 +442,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   volatile int *abort = &c.abort;
   PgWalk w(a, blockIdx.x);
 
-  if (warp == 0) {
-    // ------------------------------------------------------ score-GEMM issuer
+  if (warp == 0 || (Cfg::kQkW == 2 && warp == 2)) {
+    // ------------------------------------------------------ score-GEMM issuers
+    // (two: one for the even tiles and one for the odd)
+    const int me = warp >> 1;
     if (lane == 0) {
       constexpr uint32_t id = idesc_e4m3(128, kPgTile, 0, 0);
       const uint64_t dqr = smem_desc(smem_u32(sQr), 16, 512, kSwz64);
@@ -468,6 +460,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           break;
         }
         for (int t = w.t0; t < w.t1; ++t, ++j) {
+          if (Cfg::kQkW == 2 && (j & 1) != (uint32_t)me) continue;
           const uint32_t slot = j % NS, dS = tS + (j & 1) * kPgTile;
           if ((j >= 2 && !mbar_wait(&c.s_free[j & 1], ((j >> 1) - 1) & 1, abort, a.status)) ||
               !mbar_wait(&c.full[slot], (j / NS) & 1, abort, a.status)) {
@@ -492,12 +485,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         ++piece;
       }
       if (!ok) {
-        mma_commit(&c.drain[0]);
-        pg_drain(&c.drain[0], 0, kWaitLimitNs);
+        mma_commit(&c.drain[warp]);
+        pg_drain(&c.drain[warp], 0, kWaitLimitNs);
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 2) {
+  } else if (warp < 3) {
     // ------------------------------------------------------ PV-GEMM issuers
     // (a thread gets an MMA out every 75-100 cycles, the tensor core takes 48).
     // Loops here and at the edges stay rolled: all warps' code together is more
@@ -527,7 +520,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           tc_fence_after();
 #pragma unroll 1
-          for (int ch = me; ch < 4; ch += 2) {
+          for (int ch = me; ch < 4; ch += Cfg::kPvW) {
             const uint64_t da = dr + ((j % NS * kPgTileBytes + ch * kPgSlot) >> 4);
             uint32_t acc = t > w.t0 ? 1u : 0u;
 #pragma unroll 1
@@ -547,8 +540,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         ++piece;
       }
       if (!ok) {
-        mma_commit(&c.drain[1 + me]);
-        pg_drain(&c.drain[1 + me], 0, kWaitLimitNs);
+        mma_commit(&c.drain[warp]);
+        pg_drain(&c.drain[warp], 0, kWaitLimitNs);
       }
     }
     __syncwarp();
@@ -619,32 +612,44 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const bool live = q4 * 16 < R;  // the warp has rows
     bool ok = true;
     uint32_t j = 0, piece = 0;
-    while (w.next(a)) {
-      const bool some = w.t1 > w.t0;  // else a group that sees no key
-      const int32_t *row = a.table + (int64_t)w.m.req * a.stride;
-      const bool mine = r < w.m.count * a.hc;
-      int lo = 1, hi = 0;
+    // a piece's bounds for this thread's row, and what its first tile needs; asked
+    // for before the output of the piece ahead
+    const int32_t *row = nullptr;
+    bool mine = false;
+    int lo = 1, hi = 0, x = 0, e_cur = -1, b_nxt = -1;
+    // group g of 16 keys of tile y (lane g and its copies): its block's stored
+    // exponent, or -1 where no row may look; the block of this warpgroup's next
+    // tile's group is fetched a tile ahead of its exponent
+    auto block_at = [&](int y) {
+      const int p = ((w.m.t_lo + y) << kPgTileLog) + (lane & 3) * 16;
+      if (y >= w.t1 || p + 15 < w.m.lo_min || p > w.m.hi_max) return -1;
+      const int blk = row[p >> a.shift];
+      if (blk < 0 || blk >= a.n_blocks) {
+        record_status(a.status, CPMLA_ERR_INDEX);
+        return -1;
+      }
+      return blk;
+    };
+    auto exp_of_block = [&](int blk) { return blk >= 0 ? min((int)__ldg(a.exp + blk), 254) : -1; };
+    auto begin = [&] {
+      row = a.table + (int64_t)w.m.req * a.stride;
+      mine = r < w.m.count * a.hc;
+      lo = 1;
+      hi = 0;
       if (mine) {
         const int i = w.m.first + r / a.hc;
         lo = a.kv_lo ? max(a.kv_lo[i], 0) : 0;
         hi = a.kv_hi ? min(a.kv_hi[i], a.pos[i]) : a.pos[i];
       }
-      // group g of 16 keys of tile x (lane g and its copies): its block's stored
-      // exponent, or -1 where no row may look; the block of this warpgroup's next
-      // tile's group is fetched a tile ahead of its exponent
-      auto block_at = [&](int x) {
-        const int p = ((w.m.t_lo + x) << kPgTileLog) + (lane & 3) * 16;
-        if (x >= w.t1 || p + 15 < w.m.lo_min || p > w.m.hi_max) return -1;
-        const int blk = row[p >> a.shift];
-        if (blk < 0 || blk >= a.n_blocks) {
-          record_status(a.status, CPMLA_ERR_INDEX);
-          return -1;
-        }
-        return blk;
-      };
-      auto exp_of_block = [&](int blk) { return blk >= 0 ? min((int)__ldg(a.exp + blk), 254) : -1; };
-      int x = w.t0 + ((j & 1) == (uint32_t)wg ? 0 : 1);  // this warpgroup's first tile
-      int e_cur = exp_of_block(block_at(x)), b_nxt = block_at(x + 2);
+      x = w.t0 + ((j & 1) == (uint32_t)wg ? 0 : 1);  // this warpgroup's first tile
+      const int b0 = block_at(x);
+      b_nxt = block_at(x + 2);
+      e_cur = exp_of_block(b0);
+    };
+    bool more = w.next(a);
+    if (more) begin();
+    while (more) {
+      const bool some = w.t1 > w.t0;  // else a group that sees no key
       if (ok && some)
         ok = warp_wait(&c.q_full[piece & 1], (piece >> 1) & 1, lane, abort, a.status);
       const float qf = ok && some && mine ? c.qf[piece & 1][r] : 0.f;
@@ -744,9 +749,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           m_hi = fmaxf(m_hi, um);
           const float d = um - m_old;  // +inf at a row's first key
           if (d > 15.75f)
-            m_new = um - 10.f;
-          else if (d < 4.f)
-            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) - 10.f);
+            m_new = um - 8.f;
+          else if (d < 0.f)
+            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) - 8.f);
         }
         if (live && lane < 16) {
           c.m_ref[r] = m_new;
@@ -830,6 +835,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       j += w.t1 - w.t0;
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       // ---------------------------------------------- this piece's O and LSE
+      const int r_valid = w.m.count * a.hc, h0 = w.hg * a.hc, first = w.m.first, hc = a.hc;
+      const int part = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      const bool whole = w.whole();
+      more = w.next(a);
+      if (more) begin();
       // A warp has a quarter of the channels (its TMEM lanes) and half of the rows.
       named_bar_sync(kBarAll, 256);  // both have decided their last references
       if (live && lane < 16) {
@@ -842,45 +852,44 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       tc_fence_after();
       if (ok) {
         constexpr int RH = R / 2, RS = RH < 16 ? RH : 16;
-        const int sw = warp - 4, r_valid = w.m.count * a.hc, h0 = w.hg * a.hc;
-        const bool whole = w.whole();
+        const int sw = warp - 4;
         if (lane < RH) {
           const int rr = wg * RH + lane;
           const float m = c.m_ref[rr], sl = c.stat_l[0][rr] + c.stat_l[1][rr];
           const bool empty = m == -INFINITY && sl == 0.f;  // l may be NaN
           const float l2 = empty ? -INFINITY : m + log2f(sl);
           float f = empty ? 0.f : 1.f / sl;
-          uint8_t *optr = nullptr;
+          int64_t orow = -1;
           if (rr < r_valid) {
             if (whole) {
-              const int hh = h0 + rr % a.hc, i = w.m.first + rr / a.hc;
+              const int hh = h0 + rr % hc, i = first + rr / hc;
               const float L = l2 * 0.69314718055994530942f;
               f *= sink_factor(a.sink, hh, L);
-              const int64_t orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
-              optr = reinterpret_cast<uint8_t *>(a.o + orow * CPMLA_DV);
+              orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
               if (q4 == 0) a.lse[orow] = L;
-            } else {
-              const int64_t orow = (int64_t)(2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * R + rr;
-              optr = reinterpret_cast<uint8_t *>(a.o_part + orow * CPMLA_DV);
-              if (q4 == 0) a.lse_part[orow] = l2;
+            } else if (q4 == 0) {
+              a.lse_part[(int64_t)part * R + rr] = l2;
             }
           }
           c.inv[sw][lane] = f;
-          c.optr[sw][lane] = optr;
+          c.orow[sw][lane] = orow;
         }
         __syncwarp();
-        const int odd = lane & 1, t = q4 * 32 + lane;
-        // RS rows (columns of O^T) of a channel chunk at a time
+        const int t = q4 * 32 + lane;
+        // RS rows (columns of O^T) of a channel chunk at a time; a warp's 32 lanes
+        // are 32 channels of a row side by side.  A part's rows lie behind one
+        // another, and so do RS heads of a token where Hc is a multiple of RS:
+        // one address and constant offsets.
+        const bool dense = hc % RS == 0;
 #pragma unroll 1
         for (int cb = 0; cb < RH && wg * RH + cb < r_valid; cb += RS) {
           float f[RS];
-          uint8_t *p[RS / 2];  // rows cb + 2 y + odd
 #pragma unroll
           for (int y = 0; y < RS; ++y) f[y] = c.inv[sw][cb + y];
-#pragma unroll
-          for (int y = 0; y < RS / 2; ++y) p[y] = c.optr[sw][cb + 2 * y + odd];
+          __nv_bfloat16 *po = a.o + c.orow[sw][cb] * CPMLA_DV + t;
+          float *pp = a.o_part + ((int64_t)part * R + wg * RH + cb) * CPMLA_DV + t;
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
+          for (int ch = 0; ch < 4; ++ch, po += 128, pp += 128) {
             float o[RS];
             if (some) {
               float w3[Cfg::kWide][RS];
@@ -905,23 +914,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             }
 #pragma unroll
             for (int y = 0; y < RS; ++y) o[y] *= f[y];
-            // lane pairs trade one value: the even lane has row 2 y at channels
-            // t, t + 1, the odd lane row 2 y + 1 at t - 1, t
+            if (!whole) {
 #pragma unroll
-            for (int y = 0; y < RS / 2; ++y) {
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? o[2 * y] : o[2 * y + 1], 1);
-              o[2 * y] = odd ? got : o[2 * y];
-              o[2 * y + 1] = odd ? o[2 * y + 1] : got;
-            }
-            if (whole) {
+              for (int y = 0; y < RS; ++y) pp[y * CPMLA_DV] = o[y];
+            } else if (dense) {
 #pragma unroll
-              for (int y = 0; y < RS / 2; ++y)
-                st_global_if(p[y], p[y] + ch * 256 + (t & ~1) * 2,
-                             pack_bf16x2(o[2 * y], o[2 * y + 1]));
+              for (int y = 0; y < RS; ++y) po[y * CPMLA_DV] = __float2bfloat16_rn(o[y]);
             } else {
+#pragma unroll 1
+              for (int y = 0; y < RS; ++y) {
+                // (o by a selected register: y is not a constant here)
+                float v = o[0];
 #pragma unroll
-              for (int y = 0; y < RS / 2; ++y)
-                st_global_if(p[y], p[y] + ch * 512 + (t & ~1) * 4, o[2 * y], o[2 * y + 1]);
+                for (int z = 1; z < RS; ++z) v = z == y ? o[z] : v;
+                const int64_t orow = c.orow[sw][cb + y];
+                if (orow >= 0) a.o[orow * CPMLA_DV + ch * 128 + t] = __float2bfloat16_rn(v);
+              }
             }
           }
         }
