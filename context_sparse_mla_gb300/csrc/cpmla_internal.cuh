@@ -122,6 +122,15 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
+// --- programmatic launches: the next grid of the stream may be set up from here
+// on; wait until the grid before has ended and its writes are seen
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // --- TMA (tiled, 2D) global -> shared, completion on an mbarrier
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *tm, int x, int y,
                                             uint64_t *bar) {

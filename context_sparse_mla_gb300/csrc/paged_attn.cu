@@ -13,13 +13,14 @@
 //   * p_j = 2^(u_j - m), as fp16, is the sum of three E5M2: 9 significant bits
 //     (a bf16 has 8) where p >= 2^-8, and at worst 2^-17 off below.  m follows
 //     each tile's maximum both ways: it moves when the tile's largest p leaves
-//     [2^0, 2^15.75], to make it 2^8, so weights keep their 9 bits down to 2^-8 of
-//     a tile's own largest one at least (2^-16 where m was just set), whatever the
-//     other tiles hold.  (A first token with almost all of the weight and next to
-//     no value is common; two E4M3 terms, which need a third fewer MMAs, reach
-//     2^-9 and lose the tokens beside it.)  A move rescales O^T, a few thousand
-//     cycles, hence the wide window.  m stays within 2^60 of its highest value,
-//     beyond which a tile adds nothing.
+//     [2^-4, 2^15.75], to make it 2^6, so a weight is off by at most 2^-13 of its
+//     tile's own largest one (2^-23 where m was just set), whatever the other
+//     tiles hold.  (A first token with almost all of the weight and next to no
+//     value is common; two E4M3 terms, which need a third fewer MMAs, reach 2^-9
+//     and lose the tokens beside it.)  A move rescales O^T, a few thousand
+//     cycles, hence the wide window: with [2^4, 2^15.75] some CTAs of a 32-row
+//     decode moved 60 times and took 391 us where the others took 235.  m stays
+//     within 2^60 of its highest value, beyond which a tile adds nothing.
 // One CTA works on R = 64 rows (G tokens of one request x Hc heads) and 128
 // keys at a time, as the dense kernel does:
 //   S^T = C . [h | l]^T   M = 128 keys, N = 128, K = 576 (kind::f8f6f4), into
@@ -53,6 +54,7 @@ constexpr int kPgTileLog = 6;     // 64 keys a tile
 constexpr int kPgUnitTail = 12;   // a group's fixed cost, in tiles (plan)
 constexpr int kPgMinUnits = 8;    // tile units worth a CTA of its own
 constexpr int kPgPlanThreads = 1024;
+constexpr int kPgEarly = 4096;    // entries up to which the attention is launched early
 
 struct PagedArgs {
   const __nv_bfloat16 *q;
@@ -121,6 +123,7 @@ __device__ __forceinline__ long long pg_scan(long long v, int lane) {
 // group; CTA c starts at unit floor(total c / n).  One CTA: the entries go by in
 // rounds through shared memory, and thread c looks up CTA c's start.
 __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedArgs a) {
+  grid_launch_dependents();
   __shared__ int s_b[kPgPlanThreads], s_lo[kPgPlanThreads], s_hi[kPgPlanThreads];
   __shared__ long long s_u0[kPgPlanThreads];
   __shared__ int s_nt[kPgPlanThreads];
@@ -327,6 +330,7 @@ struct PgCtrl {
   float m_ref[R], m_hi[R];
   float stat_l[2][R];
   alignas(16) float alpha[2][R];
+  uint32_t mv[2][4];  // a row quarter has a row whose reference moved
   // per softmax warp: a row's output factor and its row of the output (-1: none)
   alignas(16) float inv[8][R / 2];
   int64_t orow[8][R / 2];
@@ -395,10 +399,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                       const __grid_constant__ CUtensorMap tm_rope) {
   using Cfg = PgCfg<R>;
   constexpr int NS = Cfg::kSlots;
-  {
-    const int4 s = a.start[blockIdx.x], e = a.start[blockIdx.x + 1];
-    if (s.x == e.x && s.y == e.y && s.z == e.z) return;  // no tiles for this CTA
-  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sQr = smem;                    // q's rope (the MMA reads 128 lanes; those behind
@@ -433,9 +433,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     tma_prefetch_desc(&tm_lat);
     tma_prefetch_desc(&tm_rope);
   }
+  grid_launch_dependents();  // the join may be set up; it waits for this grid's end
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();  // the plan is there
   const uint32_t tmem = c.tmem_base;
   // columns: q [0, 128), S buffer b at tS + 64 b, O^T chunk ch at tO + kOW ch
   const uint32_t tS = tmem + 128, tO = tS + 2 * kPgTile;
@@ -749,9 +751,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           m_hi = fmaxf(m_hi, um);
           const float d = um - m_old;  // +inf at a row's first key
           if (d > 15.75f)
-            m_new = um - 8.f;
-          else if (d < 0.f)
-            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) - 8.f);
+            m_new = um - 6.f;
+          else if (d < -4.f)
+            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) - 6.f);
         }
         if (live && lane < 16) {
           c.m_ref[r] = m_new;
@@ -763,22 +765,35 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           m_own = m_new;
         }
         if (x > w.t0 && named_bar_or(bar_wg, 128, m_new != m_old)) {
+          // only row quarters (a warp's 16 columns of O^T) in which a row moved
+          const uint32_t mv = __ballot_sync(0xffffffffu, m_new != m_old);
           if (live && lane < 16)
             c.alpha[wg][r] = m_old == -INFINITY ? 0.f : fast_exp2(m_old - m_new);
+          if (lane == 0) c.mv[wg][q4] = mv;
           named_bar_sync(bar_wg, 128);
           // the PV GEMM of the tile before is done with O^T
           if (ok) ok = warp_wait(&c.p_free[wg ^ 1], ((jj - 1) >> 1) & 1, lane, abort, a.status);
           tc_fence_after();
           if (ok) {
 #pragma unroll 1
-            for (int col = 0; col < 4 * Cfg::kOW; col += 16) {
-              float o[16];
-              tmem_ld16(tO + lane_off + col, o);
-              tmem_ld_wait();
+            for (int qr = 0; qr < R / 16; ++qr) {
+              if (c.mv[wg][qr] == 0) continue;
+#pragma unroll 1
+              for (int cc = 0; cc < 4 * Cfg::kWide; cc += 2) {  // two at a time
+                float o[2][16];
+                const uint32_t col = tO + lane_off + cc * R + qr * 16;
+                tmem_ld16(col, o[0]);
+                tmem_ld16(col + R, o[1]);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                o[i] = o[i] == 0.f ? 0.f : o[i] * c.alpha[wg][(col % R) + i];
-              tmem_st16(tO + lane_off + col, o);
+                for (int i = 0; i < 16; ++i) {
+                  const float al = c.alpha[wg][qr * 16 + i];
+                  o[0][i] = o[0][i] == 0.f ? 0.f : o[0][i] * al;
+                  o[1][i] = o[1][i] == 0.f ? 0.f : o[1][i] * al;
+                }
+                tmem_st16(col, o[0]);
+                tmem_st16(col + R, o[1]);
+              }
             }
             tmem_st_wait();
           }
@@ -1061,71 +1076,80 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 }
 
 // ------------------------------------------------------------------ the join
-// Every row of every group in the plan's joins, a CTA a row: from its parts, in
-// CTA order, each weighted by 2^(its LSE - the largest); thread t has channels
-// 4 t .. 4 t + 3.  The parts were just written, so what takes time is the chain of
-// loads: the first eight parts' values are fetched beside their LSE.
-constexpr int kPgJoinCtas = 152 * 9, kPgAhead = 8;
+// Every row of every group in the plan's joins, a warp a row: from its parts, in
+// CTA order, each weighted by 2^(its LSE - the largest); lane t has channels 128 k
+// + 4 t .. + 3.  The parts were just written and lie in L2, so what takes time is
+// the chain of loads: the first parts' values are fetched beside the LSE.
+constexpr int kPgJoinThreads = 256, kPgJoinCtas = 152 * 8, kPgAhead = 2;
 template <int R>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
-  __shared__ float s_w[kPgMaxCtas];
-  const int t = threadIdx.x, lane = t & 31;
+__global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedArgs a) {
+  grid_dependency_wait();
+  constexpr int kL = (kPgMaxCtas + 31) / 32;
+  const int lane = threadIdx.x & 31;
   const int work = a.joins[0].x * R;
-  for (int x = blockIdx.x; x < work; x += gridDim.x) {
+  for (int x = (blockIdx.x * kPgJoinThreads + threadIdx.x) >> 5; x < work;
+       x += gridDim.x * (kPgJoinThreads / 32)) {
     const int4 jn = a.joins[1 + 2 * (x / R)], jg = a.joins[2 + 2 * (x / R)];
     const int r = x % R, n = jn.w;
+    if (r >= jg.y) continue;
     // part 0 is CTA jn.z's second, part i the first of CTA jn.z + i
     auto at = [&](int i) { return (int64_t)(2 * (jn.z + i) + (i == 0 ? 1 : 0)) * R + r; };
-    auto value = [&](int i) {
-      return __ldcg(reinterpret_cast<const float4 *>(a.o_part + at(i) * CPMLA_DV) + t);
+    float4 v[kPgAhead][4];
+    auto fetch = [&](int i, float4 *d) {
+      const float4 *src = reinterpret_cast<const float4 *>(a.o_part + at(i) * CPMLA_DV) + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = __ldcg(src + 32 * k);
     };
-    if (r >= jg.y) continue;
+#pragma unroll
+    for (int i = 0; i < kPgAhead; ++i) fetch(i < n ? i : n - 1, v[i]);
     const int i = jg.x + r / a.hc, h = jn.y * a.hc + r % a.hc;
     const int64_t tok = a.tokens ? a.tokens[i] : i;
-    float4 v[kPgAhead];
+    float p[kL], mx = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPgAhead; ++i)
-      v[i] = i < n ? value(i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float p[(kPgMaxCtas + 31) / 32], mx = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < (kPgMaxCtas + 31) / 32; ++k) {
-      const int i = lane + 32 * k;
-      p[k] = i < n ? __ldcg(a.lse_part + at(i)) : -INFINITY;
+    for (int k = 0; k < kL; ++k) {
+      p[k] = lane + 32 * k < n ? __ldcg(a.lse_part + at(lane + 32 * k)) : -INFINITY;
       mx = fmaxf(mx, p[k]);
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    __syncthreads();  // the row before is done with the weights
 #pragma unroll
-    for (int k = 0; k < (kPgMaxCtas + 31) / 32; ++k) {
-      const int i = lane + 32 * k;
-      const float wt = p[k] == -INFINITY ? 0.f : exp2f(p[k] - mx);  // NaN stays
-      if (i < kPgMaxCtas && t < 32) s_w[i] = wt;
-      l += wt;
+    for (int k = 0; k < kL; ++k) {
+      p[k] = p[k] == -INFINITY ? 0.f : exp2f(p[k] - mx);  // NaN stays
+      l += p[k];
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    __syncthreads();
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < n; i0 += kPgAhead) {
 #pragma unroll
-      for (int i = 0; i < kPgAhead; ++i) {
-        const float wt = i0 + i < n ? s_w[i0 + i] : 0.f;
-        o.x = fmaf(wt, v[i].x, o.x);
-        o.y = fmaf(wt, v[i].y, o.y);
-        o.z = fmaf(wt, v[i].z, o.z);
-        o.w = fmaf(wt, v[i].w, o.w);
-      }
+      for (int y = 0; y < kPgAhead; ++y) {
+        const int ii = i0 + y;
+        float wt = p[0];
 #pragma unroll
-      for (int i = 0; i < kPgAhead; ++i)
-        if (i0 + kPgAhead + i < n) v[i] = value(i0 + kPgAhead + i);
+        for (int k = 1; k < kL; ++k) wt = ii >> 5 == k ? p[k] : wt;
+        wt = __shfl_sync(0xffffffffu, wt, ii & 31);
+        if (ii >= n) wt = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[k].x = fmaf(wt, v[y][k].x, o[k].x);
+          o[k].y = fmaf(wt, v[y][k].y, o[k].y);
+          o[k].z = fmaf(wt, v[y][k].z, o[k].z);
+          o[k].w = fmaf(wt, v[y][k].w, o[k].w);
+        }
+        if (ii + kPgAhead < n) fetch(ii + kPgAhead, v[y]);
+      }
     }
     const bool empty = mx == -INFINITY && l == 0.f;  // l may be NaN
     const float L = empty ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
     const float f = empty ? 0.f : sink_factor(a.sink, h, L) / l;
-    reinterpret_cast<uint2 *>(a.o + (tok * a.H + h) * CPMLA_DV)[t] =
-        make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-    if (t == 0) a.lse[tok * a.H + h] = L;
+    uint2 *dst = reinterpret_cast<uint2 *>(a.o + (tok * a.H + h) * CPMLA_DV) + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      dst[32 * k] = make_uint2(pack_bf16x2(o[k].x * f, o[k].y * f),
+                               pack_bf16x2(o[k].z * f, o[k].w * f));
+    if (lane == 0) a.lse[tok * a.H + h] = L;
   }
 }
 
@@ -1158,11 +1182,29 @@ int launch_paged(const PagedArgs &a, const CUtensorMap &tm_lat, const CUtensorMa
   if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: set shared memory size");
   paged_plan_kernel<<<1, kPgPlanThreads, 0, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: plan launch");
-  paged_attn_kernel<R><<<a.n_cta, kPgThreads, pg_smem<R>(), st>>>(a, tm_lat, tm_rope);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: launch");
+  // The other two may start while the kernel ahead of them still runs (their setup
+  // beside its end) and wait for its end before they read what it wrote.  The
+  // attention does so for up to kPgEarly entries: with 2,500 it takes 470 us
+  // instead of 487; with 8,192, where the plan takes 30 us, 1,338 instead of 1,217.
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.attrs = &at;
+  cfg.numAttrs = a.n <= kPgEarly ? 1 : 0;
+  cfg.stream = st;
+  cfg.gridDim = dim3(a.n_cta);
+  cfg.blockDim = dim3(kPgThreads);
+  cfg.dynamicSmemBytes = pg_smem<R>();
+  e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<R>, a, tm_lat, tm_rope);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: launch");
   if (a.n_cta > 1) {
-    paged_join_kernel<R><<<kPgJoinCtas, 128, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: join launch");
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(kPgJoinCtas);
+    cfg.blockDim = dim3(kPgJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel<R>, a);
+    if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: join launch");
   }
   return CPMLA_OK;
 }
