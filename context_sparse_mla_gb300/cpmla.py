@@ -8,7 +8,6 @@ missing the import of a function fails loudly -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -324,36 +323,52 @@ def lse_merge_with_sink(o_part, lse_part, contrib_rows, o_out, lse_out, *, contr
 
 
 # ------------------------------------------------------- the paged 8-bit cache
-def _on_device_of(fn):
-    """Run fn with its first tensor argument's device current, so that the
-    library's status word, stream and kernels are that device's; the other
-    tensors must lie there too."""
-    @functools.wraps(fn)
-    def call(first, *args, **kw):
-        tensors = [x for x in (first, *args, *kw.values(), *(kw.get("out") or {}).values())
-                   if isinstance(x, torch.Tensor)]
-        if not all(x.device == first.device for x in tensors):
-            raise ValueError("the tensors are on different devices")
-        if not first.is_cuda:
-            raise ValueError("the tensors must be on a CUDA device")
-        with torch.cuda.device(first.device):
-            return fn(first, *args, **kw)
-    return call
+# These calls are short (a step's maps take the GPU 5 us), so their checks are one
+# comparison each and pointers go to the library as plain integers.
+def _at(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor of this type, shape (None: any) and device."""
+    if (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
+        raise ValueError("%s must be a contiguous %s tensor%s on cuda:%d, got %s %s on %s"
+                         % (name, dtype, "" if shape is None else " " + str(list(shape)), dev,
+                            t.dtype, list(t.shape), t.device))
+    return t.data_ptr()
 
 
-def _shaped(t, dtype, name, shape):
-    _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    return t
+def _opt_at(t, dtype, shape, dev, name):
+    return None if t is None else _at(t, dtype, shape, dev, name)
 
 
-def _paged_cache(cache, cache_exp):
-    _dev(cache, torch.uint8, "cache")
+def _launch(fn, dev, stream, *args):
+    """Call an entry point on a device, which is made current for it: the
+    library's status word, its launches and the stream are that device's."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, *args)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    else:
+        raw = stream.cuda_stream
+    rc = fn(*args, raw)
+    if rc != CPMLA_OK:
+        _check(rc)
+
+
+def _cuda_index(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be on a CUDA device" % name)
+    return dev
+
+
+def _paged_cache(cache, cache_exp, dev):
     if cache.dim() != 3 or cache.shape[2] != DQK:
         raise ValueError("cache must be [n_blocks, block_size, 576]")
-    _shaped(cache_exp, torch.uint8, "cache_exp", cache.shape[:1])
-    return cache.shape[0], cache.shape[1]
+    nb, bs = cache.shape[0], cache.shape[1]
+    return (nb, bs, _at(cache, torch.uint8, None, dev, "cache"),
+            _at(cache_exp, torch.uint8, (nb,), dev, "cache_exp"))
 
 
 def paged_maps_out(B, n_slots, device="cuda"):
@@ -364,7 +379,6 @@ def paged_maps_out(B, n_slots, device="cuda"):
                 free_head=e(1, torch.int32))
 
 
-@_on_device_of
 def mla_paged_maps(ctx_len, new_len, free_blocks, block_table, *, block_size, n_blocks,
                    n_slots=None, free_head=None, out=None, stream=None):
     """Block tables and slot maps of a step from request lengths (int32 [B]):
@@ -374,47 +388,41 @@ def mla_paged_maps(ctx_len, new_len, free_blocks, block_table, *, block_size, n_
     given, else for n_slots entries) of cu_seqlens [B + 1], slot_mapping
     int64, pos and req int32 [n_slots] (-1 behind the last token) and free_head
     [1], the count taken so far."""
-    _dev(ctx_len, torch.int32, "ctx_len")
-    B = ctx_len.numel()
-    _shaped(new_len, torch.int32, "new_len", (B,))
-    _dev(free_blocks, torch.int32, "free_blocks")
-    _dev(block_table, torch.int32, "block_table")
+    dev = _cuda_index(ctx_len, "ctx_len")
+    B, i32 = ctx_len.numel(), torch.int32
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [%d, width]" % B)
-    if free_head is not None:
-        _shaped(free_head, torch.int32, "free_head", (1,))
     if out is None:
         if n_slots is None:
             raise ValueError("n_slots or out is needed")
         out = paged_maps_out(B, n_slots, ctx_len.device)
-    n_slots = out["slot_mapping"].numel()
-    _check(lib().mla_paged_maps(
-        _ptr(ctx_len), _ptr(new_len), B, int(block_size), int(n_blocks), _ptr(free_blocks),
-        free_blocks.numel(), _ptr(free_head), _ptr(block_table), block_table.shape[1], n_slots,
-        _ptr(_shaped(out["cu_seqlens"], torch.int32, "cu_seqlens", (B + 1,))),
-        _ptr(_shaped(out["slot_mapping"], torch.int64, "slot_mapping", (n_slots,))),
-        _ptr(_shaped(out["pos"], torch.int32, "pos", (n_slots,))),
-        _ptr(_shaped(out["req"], torch.int32, "req", (n_slots,))),
-        _ptr(_shaped(out["free_head"], torch.int32, "free_head", (1,))), _stream(stream)))
+    n = out["slot_mapping"].numel()
+    _launch((_lib or lib()).mla_paged_maps, dev, stream,
+            _at(ctx_len, i32, (B,), dev, "ctx_len"), _at(new_len, i32, (B,), dev, "new_len"), B,
+            block_size, n_blocks, _at(free_blocks, i32, None, dev, "free_blocks"),
+            free_blocks.numel(), _opt_at(free_head, i32, (1,), dev, "free_head"),
+            _at(block_table, i32, None, dev, "block_table"), block_table.shape[1], n,
+            _at(out["cu_seqlens"], i32, (B + 1,), dev, "cu_seqlens"),
+            _at(out["slot_mapping"], torch.int64, (n,), dev, "slot_mapping"),
+            _at(out["pos"], i32, (n,), dev, "pos"), _at(out["req"], i32, (n,), dev, "req"),
+            _at(out["free_head"], i32, (1,), dev, "free_head"))
     return out
 
 
-@_on_device_of
 def mla_paged_cache_insert(kv, slot_mapping, cache, cache_exp, *, stream=None):
     """Write each token's latent KV row (kv [n, 576] bf16) to slot
     slot_mapping[t] (int64, -1 skips) of the paged 8-bit cache, in place: cache
     uint8 [n_blocks, block_size, 576] of E4M3 codes and cache_exp uint8
     [n_blocks], the exponent (+ 127) of each block's scale.  The tokens of one
     block stand side by side."""
-    nb, bs = _paged_cache(cache, cache_exp)
-    if not (kv.is_cuda and kv.dtype == torch.bfloat16 and kv.dim() == 2 and kv.shape[1] == DQK
-            and kv.stride(1) == 1):
-        raise ValueError("kv must be a CUDA bfloat16 [n, 576] tensor with contiguous rows")
+    dev = _cuda_index(kv, "kv")
+    nb, bs, pc, pe = _paged_cache(cache, cache_exp, dev)
+    if kv.dtype is not torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != DQK or kv.stride(1) != 1:
+        raise ValueError("kv must be a bfloat16 [n, 576] tensor with contiguous rows")
     n = kv.shape[0]
-    _check(lib().mla_paged_cache_insert(
-        _ptr(kv), kv.stride(0) if n > 1 else DQK, n,
-        _ptr(_shaped(slot_mapping, torch.int64, "slot_mapping", (n,))), _ptr(cache),
-        _ptr(cache_exp), nb, bs, _stream(stream)))
+    _launch((_lib or lib()).mla_paged_cache_insert, dev, stream, kv.data_ptr(),
+            kv.stride(0) if n > 1 else DQK, n,
+            _at(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), pc, pe, nb, bs)
 
 
 def paged_attn_workspace(H, n_tokens, device="cuda"):
@@ -424,7 +432,6 @@ def paged_attn_workspace(H, n_tokens, device="cuda"):
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
 
 
-@_on_device_of
 def mla_paged_attn(q, cache, cache_exp, block_table, pos, req, o_out, lse_out, *, softmax_scale,
                    workspace, tokens=None, sink=None, kv_lo=None, kv_hi=None, stream=None):
     """Attention of the listed entries over the paged 8-bit cache: entry i is
@@ -432,28 +439,27 @@ def mla_paged_attn(q, cache, cache_exp, block_table, pos, req, o_out, lse_out, *
     req -1 stands for no token), causal and within [kv_lo[i], kv_hi[i]] when
     given.  q [T, H, 576] bf16 (tokens may be strided); writes the entries'
     rows of o_out [T, H, 512] bf16 (sink applied once) and lse_out [T, H]."""
-    nb, bs = _paged_cache(cache, cache_exp)
-    if not (q.is_cuda and q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[2] == DQK
-            and q.stride(2) == 1 and (q.stride(1) == DQK or q.shape[1] == 1)):
-        raise ValueError("q must be a CUDA bfloat16 [T, H, 576] tensor with contiguous tokens")
-    T, H = q.shape[0], q.shape[1]
-    n = pos.numel()
-    _dev(block_table, torch.int32, "block_table")
+    dev = _cuda_index(q, "q")
+    nb, bs, pc, pe = _paged_cache(cache, cache_exp, dev)
+    if (q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != DQK or q.stride(2) != 1
+            or (q.shape[1] != 1 and q.stride(1) != DQK)):
+        raise ValueError("q must be a bfloat16 [T, H, 576] tensor with contiguous tokens")
+    T, H, _ = q.shape
+    n, i32 = pos.numel(), torch.int32
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, width]")
     if tokens is None and n > T:
         raise ValueError("%d entries for %d tokens: give their tokens" % (n, T))
-    opt = lambda t, name: None if t is None else _shaped(t, torch.int32, name, (n,))
-    _check(lib().mla_paged_attn(
-        _ptr(q), q.stride(0) if T > 1 else H * DQK, H, _ptr(cache), _ptr(cache_exp), nb, bs,
-        _ptr(block_table), block_table.shape[0], block_table.shape[1],
-        _ptr(opt(tokens, "tokens")), _ptr(_shaped(pos, torch.int32, "pos", (n,))),
-        _ptr(_shaped(req, torch.int32, "req", (n,))), n, _ptr(opt(kv_lo, "kv_lo")),
-        _ptr(opt(kv_hi, "kv_hi")), float(softmax_scale),
-        None if sink is None else _ptr(_shaped(sink, torch.float32, "sink", (H,))), T,
-        _ptr(_shaped(o_out, torch.bfloat16, "o_out", (T, H, DV))),
-        _ptr(_shaped(lse_out, torch.float32, "lse_out", (T, H))),
-        _ptr(_dev(workspace, torch.uint8, "workspace")), workspace.numel(), _stream(stream)))
+    _launch((_lib or lib()).mla_paged_attn, dev, stream, q.data_ptr(),
+            q.stride(0) if T > 1 else H * DQK, H, pc, pe, nb, bs,
+            _at(block_table, i32, None, dev, "block_table"), block_table.shape[0],
+            block_table.shape[1], _opt_at(tokens, i32, (n,), dev, "tokens"),
+            _at(pos, i32, (n,), dev, "pos"), _at(req, i32, (n,), dev, "req"), n,
+            _opt_at(kv_lo, i32, (n,), dev, "kv_lo"), _opt_at(kv_hi, i32, (n,), dev, "kv_hi"),
+            softmax_scale, _opt_at(sink, torch.float32, (H,), dev, "sink"), T,
+            _at(o_out, torch.bfloat16, (T, H, DV), dev, "o_out"),
+            _at(lse_out, torch.float32, (T, H), dev, "lse_out"),
+            _at(workspace, torch.uint8, None, dev, "workspace"), workspace.numel())
 
 
 def device_status(clear=True):

@@ -41,6 +41,7 @@
 // softmax and the output, 12-15 bring q in.  Every wait is
 // bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains its copies and
 // MMAs, frees TMEM and exits.
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -1174,12 +1175,34 @@ int pg_rows(int hc, int n_tokens, int B) {
   return hc <= 16 ? 16 : 32;
 }
 
+// SMs of the current device (-1 on failure), with the attention's kernel for R
+// rows allowed its shared memory there; asked once a device and R.
+int pg_device(int R) {
+  constexpr int kMax = 64;
+  static std::atomic<int> known[3][kMax];
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const bool keep = e == cudaSuccess && dev >= 0 && dev < kMax;
+  std::atomic<int> &slot = known[R == 64 ? 2 : (R == 32 ? 1 : 0)][keep ? dev : 0];
+  if (keep && (sms = slot.load(std::memory_order_acquire)) > 0) return sms;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if (e == cudaSuccess)
+    e = R == 64   ? cudaFuncSetAttribute(paged_attn_kernel<64>, attr, pg_smem<64>())
+        : R == 32 ? cudaFuncSetAttribute(paged_attn_kernel<32>, attr, pg_smem<32>())
+                  : cudaFuncSetAttribute(paged_attn_kernel<16>, attr, pg_smem<16>());
+  if (e != cudaSuccess) {
+    cuda_fail(e, "mla_paged_attn: device");
+    return -1;
+  }
+  if (keep) slot.store(sms, std::memory_order_release);
+  return sms;
+}
+
 template <int R>
 int launch_paged(const PagedArgs &a, const CUtensorMap &tm_lat, const CUtensorMap &tm_rope,
                  cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<R>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, pg_smem<R>());
-  if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: set shared memory size");
+  cudaError_t e;
   paged_plan_kernel<<<1, kPgPlanThreads, 0, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "mla_paged_attn: plan launch");
   // The other two may start while the kernel ahead of them still runs (their setup
@@ -1282,10 +1305,8 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
   const int R = pg_rows(a.hc, n_tokens, B);
   a.g = R / a.hc;
   a.n_hg = H / a.hc;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "mla_paged_attn: device");
+  const int sms = pg_device(R);
+  if (sms < 0) return CPMLA_ERR_CUDA;
   a.n_cta = sms < kPgMaxCtas ? sms : kPgMaxCtas;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const PgLayout L = pg_layout(n_tokens, R);
@@ -1314,7 +1335,7 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
     if (cr != CUDA_SUCCESS)
       return fail(CPMLA_ERR_CUDA, "%s: tensor map encode failed (%d)", fn, (int)cr);
   }
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return R == 64   ? launch_paged<64>(a, tm[0], tm[1], st)
          : R == 32 ? launch_paged<32>(a, tm[0], tm[1], st)
                    : launch_paged<16>(a, tm[0], tm[1], st);
