@@ -310,6 +310,10 @@ struct PgCfg {
   static constexpr int kPvW = R == 64 ? 2 : 1, kQkW = 3 - kPvW;
   static constexpr int kQRope = 2 * R * 64;  // q's rope: [2R lanes x 64]
   static constexpr int kFixed = kQRope + 2 * kP;
+  // Steps of q (of 16) split before the wait for q's place, at 8 registers each: between
+  // the pieces of a prompt the split was 16,000 cycles of waiting (8,192 tokens of 16
+  // heads: 1,215 us with none, 1,160 with 8).  R = 16 is slower with it (247, 222 us).
+  static constexpr int kQAhead = R == 64 ? 8 : 0;
   static constexpr int kSlots = R == 16 ? 6 : 5;  // tiles in the ring
 };
 
@@ -369,24 +373,28 @@ __device__ __forceinline__ uint32_t f16x2_minus_upper(uint32_t h2) {
                             *reinterpret_cast<const __half2 *>(&up));
   return *reinterpret_cast<const uint32_t *>(&d);
 }
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h2) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
 }
-// {h, l} of two channels: h = E4M3(x), l = E4M3(16 (x - h)), two codes each
-__device__ __forceinline__ uint2 split_q(float x0, float x1) {
-  const uint32_t h = e4m3x2(x0, x1);
-  const uint32_t b = e4m3x2_to_f16x2((uint16_t)h);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&b));
-  return make_uint2(h, e4m3x2(16.f * (x0 - f.x), 16.f * (x1 - f.y)));
+// {h, l} of two channels x down (bf16 pairs): h = E4M3(x), l = E4M3(16 (x - h)), two
+// codes each.  fp16 holds x down to 2^-24, and x - h exactly; l ends at 2^-13.
+__device__ __forceinline__ uint2 split_q(uint32_t w, uint32_t down) {
+  uint32_t x, f;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w), "r"(down));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+      : "=r"(f)
+      : "f"(__uint_as_float(x & 0xFFFF0000u)), "f"(__uint_as_float(x << 16)));
+  const uint32_t h = e4m3x2_of_f16x2(f), b = e4m3x2_to_f16x2((uint16_t)h);
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(f), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x4C004C00u));  // 16
+  return make_uint2(h, e4m3x2_of_f16x2(d));
 }
-// The same of four channels (two words of bf16 pairs) times `down`.
-__device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, float down) {
-  const uint2 a = split_q(__uint_as_float(w0 << 16) * down,
-                          __uint_as_float(w0 & 0xFFFF0000u) * down);
-  const uint2 b = split_q(__uint_as_float(w1 << 16) * down,
-                          __uint_as_float(w1 & 0xFFFF0000u) * down);
+// The same of four channels.
+__device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, uint32_t down) {
+  const uint2 a = split_q(w0, down), b = split_q(w1, down);
   return make_uint2(a.x | (b.x << 16), a.y | (b.y << 16));
 }
 // 2^e for the stored exponent e + 127
@@ -1003,11 +1011,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
       }
       uint4 w[4][2];
-      if (q4 * 16 < R) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fetch(i, w[i]);
-      }
-      float down[2], up[2];
+      uint32_t down[2];
+      float up[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         uint32_t m = max(mx[x] & 0xFFFFu, mx[x] >> 16);
@@ -1017,9 +1022,39 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // keep fewer bits)
         int ae = (int)(m >> 7) - 127 - ((m & 0x7Fu) > 0x60u ? 7 : 8);
         ae = ae < -60 ? -60 : (ae > 120 ? 120 : ae);
-        down[x] = __int_as_float((127 - ae) << 23);
+        down[x] = (uint32_t)(127 - ae) * 0x00800080u;
         // a row with an infinite or NaN channel is NaN throughout
         up[x] = m >= 0x7F80u ? NAN : __int_as_float((127 + ae) << 23) * a.scale_log2;
+      }
+      // a step's words for the two stores
+      auto split = [&](const uint4 *v, uint32_t *p) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint2 p0 = split_q4(v[x].x, v[x].y, down[x]);
+          const uint2 p1 = split_q4(v[x].z, v[x].w, down[x]);
+          p[2 * x] = p0.x;
+          p[2 * x + 1] = p1.x;
+          p[4 + 2 * x] = p0.y;
+          p[5 + 2 * x] = p1.y;
+        }
+      };
+      auto put = [&](int n, const uint32_t *p) {
+        const uint32_t at = tmem + lane_off + n * 8;
+        tmem_st_16x256b_x1(at, p[0], p[1], p[2], p[3]);
+        tmem_st_16x256b_x1(at + (16u << 16), p[4], p[5], p[6], p[7]);
+      };
+      // what the registers hold is split ahead of the wait
+      uint32_t pre[Cfg::kQAhead > 0 ? Cfg::kQAhead : 1][8];
+      if (q4 * 16 < R) {
+#pragma unroll
+        for (int n = 0; n < Cfg::kQAhead; n += 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) fetch(n + i, w[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split(w[i], pre[n + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch(Cfg::kQAhead + i, w[i]);
       }
       // the softmax is done with the piece two before (its scales' place is used
       // again, and it has seen that piece's q_full), the score GEMMs with q
@@ -1031,19 +1066,15 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (c4 == 0) c.qf[k & 1][q4 * 16 + 8 * x + y8] = up[x];
+#pragma unroll
+        for (int n = 0; n < Cfg::kQAhead; ++n) put(n, pre[n]);
 #pragma unroll 1
-        for (int n = 0; n < 16; n += 4) {
+        for (int n = Cfg::kQAhead; n < 16; n += 4) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint2 p[2][2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              p[x][0] = split_q4(w[i][x].x, w[i][x].y, down[x]);
-              p[x][1] = split_q4(w[i][x].z, w[i][x].w, down[x]);
-            }
-            const uint32_t at = tmem + lane_off + (n + i) * 8;
-            tmem_st_16x256b_x1(at, p[0][0].x, p[0][1].x, p[1][0].x, p[1][1].x);
-            tmem_st_16x256b_x1(at + (16u << 16), p[0][0].y, p[0][1].y, p[1][0].y, p[1][1].y);
+            uint32_t p[8];
+            split(w[i], p);
+            put(n + i, p);
             fetch(min(n + i + 4, 17), w[i]);
           }
         }
