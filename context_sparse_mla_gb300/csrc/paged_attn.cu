@@ -21,26 +21,38 @@
 //     cycles, hence the wide window: with [2^4, 2^15.75] some CTAs of a 32-row
 //     decode moved 60 times and took 391 us where the others took 235.  m stays
 //     within 2^60 of its highest value, beyond which a tile adds nothing.
-// One CTA works on R = 64 rows (G tokens of one request x Hc heads) and 128
-// keys at a time, as the dense kernel does:
-//   S^T = C . [h | l]^T   M = 128 keys, N = 128, K = 576 (kind::f8f6f4), into
-//                         one of two TMEM buffers
-//   O^T += C^T . P^T      M = 128 channels x 4, N = 64, K = 128 keys, for the
-//                         three parts of p; 256 TMEM columns
-// The value is the latent itself: a chunk [128 keys x 128 channels] stays in
-// its 16 KB ring slot from the score GEMM to the PV GEMM, so a tile costs 72
-// KB of loads (the bf16 kernel's: 288 KB).
+// A piece of work is R = 16 or 64 rows (G tokens of one request x Hc heads) and
+// a range of their keys, 64 at a time:
+//   S = [h; l] . C^T      q (2R lanes) in TMEM, the tile's keys as N = 64, K = 576
+//                         (kind::f8f6f4; the rope's 64 from shared memory), into
+//                         one of two S buffers
+//   O^T += C^T . P^T      M = 128 channels x 4, N = R a part of p (parts side by
+//                         side where TMEM has the columns), K = 64 keys
+// The value is the latent itself: a tile's chunks [64 keys x 128 channels] stay in
+// their ring slot from the score GEMM to the PV GEMM, so 64 keys cost 36 KB of
+// loads, once for R rows (the bf16 kernel's: 144 KB), in a ring of 5 or 6 tiles.
+// Two softmax warpgroups take the tiles in turn; S rows lie on TMEM lanes, so a
+// row's threads read 32 keys each and one shuffle joins them.
 //
 // The work is cut by tiles, not by rows: a first launch (one CTA) groups the
 // entries, counts tiles and gives every SM the same number of tile units; a
 // group that is cut leaves normalised fp32 parts in the workspace, at most two
-// for each SM, and a third launch joins them in a fixed order.
+// for each SM, and a third launch joins them in a fixed order.  One request's
+// token uses up to 152 SMs that way, and lists of any mix end together.
 //
-// Warps: 0 issues the score GEMMs, 1 and 2 the PV GEMMs (R < 64: 0 and 2, and 1), 3
-// loads, 4-11 do the
-// softmax and the output, 12-15 bring q in.  Every wait is
-// bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains its copies and
-// MMAs, frees TMEM and exits.
+// Warps: 0-2 issue the MMAs (R = 64: 0 the scores, 1 and 2 PV; R = 16: 0 and 2
+// the scores, 1 PV), 3 loads, 4-11 do the softmax and the output, 12-15 bring q
+// in.  Every wait is bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains
+// its copies and MMAs, frees TMEM and exits.
+//
+// What bounds it, measured.  R = 16 (32 requests of 65,536 keys x 16 heads): HBM;
+// 224 us a call, 5.1 TB/s over the whole call, 5.6 in the kernel.  R = 64: shared
+// memory and the MMA issue.  A tile's 42 MMAs read 188 KB of it (each part of p
+// reads the 4 KB of keys again: three parts side by side would need 768 TMEM
+// columns) and the copies write 36 KB, about 1,800 cycles at 128 B a cycle; it
+// takes 2,050.  Between two pieces the tensor core stands still for about 8 tiles:
+// the last softmax and PV, the output, and q's split do not overlap the next
+// piece's.  8,192 tokens x 16 heads 1,160 us (1.00 PFLOP/s of the exact products).
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -52,8 +64,13 @@ namespace {
 
 constexpr int kPgMaxCtas = 160;   // at most one CTA per SM
 constexpr int kPgTileLog = 6;     // 64 keys a tile
-constexpr int kPgUnitTail = 12;   // a group's fixed cost, in tiles (plan)
-constexpr int kPgMinUnits = 8;    // tile units worth a CTA of its own
+// The plan's units are tiles: what a piece costs beside its tiles (8, 12 and 16 were
+// measured: 8,192 prompt tokens 1,270, 1,163 and 1,160 us, 64-head chunks 459, 442 and
+// 436), and what is worth a CTA of its own (one token of 8,192 keys: 28 us with 8, 24
+// with 4, where more parts cost the join more).
+constexpr int kPgUnitTail = 16;
+constexpr int kPgMinUnits = 4;
+constexpr int kPgLongJoin = 8;    // parts up to which a row's join is a warp's
 constexpr int kPgPlanThreads = 1024;
 constexpr int kPgEarly = 4096;    // entries up to which the attention is launched early
 
@@ -76,8 +93,9 @@ struct PagedArgs {
   int n_cta;
   struct PgGroup *groups;
   int4 *start;      // [kPgMaxCtas + 1]: (group, head group, tile) a CTA starts at
-  int4 *joins;      // a count, then two words for each group that is cut: (group, head group,
-                    // first CTA, parts), (first entry, rows, -, -)
+  int4 *joins;      // counts of short and long ones, then two words for each group that is
+                    // cut: (group, head group, first CTA, parts), (first entry, rows, -, -);
+                    // short ones from the front, those of many parts from the back
   float *o_part;    // [2 kPgMaxCtas][R][512]
   float *lse_part;  // [2 kPgMaxCtas][R], base 2
   int *status;
@@ -229,32 +247,40 @@ __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedA
   static_assert(kPgMaxCtas <= 5 * 32, "five warps look for cuts");
   if (warp < 5) {
     const int c = tid + 1;
+    const int4 st = s_start[c], p = s_start[c - 1];
+    const bool in = st.z > 0, cont = in && p.z > 0 && p.x == st.x && p.y == st.y;
+    const uint32_t b = __ballot_sync(0xffffffffu, cont);
+    if (lane == 0) s_n[warp] = (int)b;
+    named_bar_sync(1, 160);
     int parts = 0;
-    int4 st = make_int4(0, 0, 0, 0);
-    if (c <= kPgMaxCtas) {
-      st = s_start[c];
-      const int4 p = s_start[c - 1];
-      if (st.z > 0 && !(p.x == st.x && p.y == st.y && p.z > 0)) {
-        parts = 2;
-        while (c + parts - 1 <= kPgMaxCtas) {
-          const int4 x = s_start[c + parts - 1];
-          if (x.x != st.x || x.y != st.y || x.z == 0) break;
-          ++parts;
-        }
+    if (in && !cont) {  // boundaries tid + 1 .. behind it in the same piece
+      int e = tid + 1;
+      for (int x = e >> 5; x < 5; ++x) {
+        const uint32_t gone = ~(uint32_t)s_n[x] & (x == e >> 5 ? ~0u << (e & 31) : ~0u);
+        e = gone ? 32 * x + __ffs(gone) - 1 : 32 * (x + 1);
+        if (gone) break;
       }
+      parts = e - tid + 1;
     }
-    const uint32_t b = __ballot_sync(0xffffffffu, parts > 0);
-    if (lane == 0) s_n[warp] = __popc(b);
+    const bool lng = parts > kPgLongJoin;
+    const uint32_t bs = __ballot_sync(0xffffffffu, parts > 0 && !lng);
+    const uint32_t bl = __ballot_sync(0xffffffffu, lng);
+    if (lane == 0) s_n[8 + warp] = __popc(bs) | __popc(bl) << 16;
     named_bar_sync(1, 160);
     int at = 0;
-    for (int x = 0; x < warp; ++x) at += s_n[x];
-    at += __popc(b & ((1u << lane) - 1));
+    for (int x = 0; x < warp; ++x) at += s_n[8 + x];
+    const uint32_t below = (1u << lane) - 1;
     if (parts > 0) {
+      const int k = lng ? kPgMaxCtas - 1 - (at >> 16) - __popc(bl & below)
+                        : (at & 0xFFFF) + __popc(bs & below);
       const PgGroup &m = a.groups[st.x];
-      a.joins[1 + 2 * at] = make_int4(st.x, st.y, c - 1, parts);
-      a.joins[2 + 2 * at] = make_int4(m.first, m.count * a.hc, 0, 0);
+      a.joins[1 + 2 * k] = make_int4(st.x, st.y, c - 1, parts);
+      a.joins[2 + 2 * k] = make_int4(m.first, m.count * a.hc, 0, 0);
     }
-    if (tid == 159) a.joins[0] = make_int4(at + (parts > 0 ? 1 : 0), 0, 0, 0);
+    if (tid == 159) {
+      at += __popc(bs) | __popc(bl) << 16;
+      a.joins[0] = make_int4(at & 0xFFFF, at >> 16, 0, 0);
+    }
   }
 }
 
@@ -301,12 +327,12 @@ struct PgCfg {
   static constexpr int kPart = R * kPgTile;  // one part of P: [R rows x 64 keys]
   static constexpr int kP = kPgParts * kPart;
   // Parts of P side by side in one PV MMA, each with accumulators of its own (TMEM
-  // holds 4 R kWide + 256 columns): an MMA of N = 16, 32 or 64 takes 40, 40 or 48
-  // cycles, most of them for the 4 KB of keys, which N = 48 reads once for three.
-  static constexpr int kWide = R == 16 ? 3 : (R == 32 ? 2 : 1);
+  // holds 4 R kWide + 256 columns): an MMA of N = 16 takes 40 cycles and one of N = 48
+  // or 64 takes 48, most of them for the 4 KB of keys, which N = 48 reads once for three.
+  static constexpr int kWide = R == 16 ? 3 : 1;
   static constexpr int kOW = R * kWide;  // columns of an O^T chunk
   // MMA issuers (warps 0-2): R = 64 has 24 PV MMAs a tile for two threads beside the
-  // 18 of the scores, fewer rows 8 or 16 for one, and the scores two
+  // 18 of the scores, R = 16 has 8 for one, and the scores two
   static constexpr int kPvW = R == 64 ? 2 : 1, kQkW = 3 - kPvW;
   static constexpr int kQRope = 2 * R * 64;  // q's rope: [2R lanes x 64]
   static constexpr int kFixed = kQRope + 2 * kP;
@@ -344,8 +370,7 @@ template <int R>
 constexpr int pg_smem() {
   return 1024 + PgCfg<R>::kFixed + PgCfg<R>::kSlots * kPgTileBytes + (int)sizeof(PgCtrl<R>);
 }
-static_assert(pg_smem<64>() <= 232448 && pg_smem<32>() <= 232448 && pg_smem<16>() <= 232448,
-              "shared memory budget");
+static_assert(pg_smem<64>() <= 232448 && pg_smem<16>() <= 232448, "shared memory budget");
 
 constexpr unsigned long long kPgDrainNs = 20ull * 1000 * 1000;
 __device__ __forceinline__ void pg_drain(uint64_t *bar, uint32_t parity,
@@ -397,10 +422,8 @@ __device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, uint32_t dow
   const uint2 a = split_q(w0, down), b = split_q(w1, down);
   return make_uint2(a.x | (b.x << 16), a.y | (b.y << 16));
 }
-// 2^e for the stored exponent e + 127
-__device__ __forceinline__ float pg_pow2(int stored) {
-  return stored == 0 ? 5.877471754e-39f : __int_as_float(stored << 23);
-}
+// 2^e for the stored exponent e + 127, 63 .. 247
+__device__ __forceinline__ float pg_pow2(int stored) { return __int_as_float(stored << 23); }
 template <int R>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedArgs a,
@@ -641,7 +664,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       }
       return blk;
     };
-    auto exp_of_block = [&](int blk) { return blk >= 0 ? min((int)__ldg(a.exp + blk), 254) : -1; };
+    auto exp_of_block = [&](int blk) {
+      return blk >= 0 ? max(63, min((int)__ldg(a.exp + blk), 247)) : -1;
+    };
     auto begin = [&] {
       row = a.table + (int64_t)w.m.req * a.stride;
       mine = r < w.m.count * a.hc;
@@ -974,7 +999,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // q4 .., lanes 16-31 the l parts: thread 4 y + c reads 8 channels of rows y and y
     // + 8, 32 channels a step with its quad, and two 16-lane stores put the parts
     // where they belong.  The last two steps, the rope, go to shared memory.
-    // (The loops are kept short: see the MMA issuers.)
+    // (The loops are kept short: code that runs once a piece comes from L2, at
+    // about 8 cycles an instruction.)
     auto load_q = [&](const PgWalk &v, uint32_t k) {
       const int r_valid = v.m.count * a.hc, y8 = lane >> 2, c4 = lane & 3;
       const uint4 *src[2];
@@ -1108,35 +1134,37 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 }
 
 // ------------------------------------------------------------------ the join
-// Every row of every group in the plan's joins, a warp a row: from its parts, in
-// CTA order, each weighted by 2^(its LSE - the largest); lane t has channels 128 k
-// + 4 t .. + 3.  The parts were just written and lie in L2, so what takes time is
-// the chain of loads: the first parts' values are fetched beside the LSE.
-constexpr int kPgJoinThreads = 256, kPgJoinCtas = 152 * 8, kPgAhead = 2;
+// A row of a join (group, head group, first CTA, parts) from its parts, in an order
+// that the plan alone decides, each weighted by 2^(its LSE - the largest); lane t has
+// channels 128 k + 4 t .. + 3.  The parts were just written and lie in L2, so what
+// takes time is the chain of loads: kAhead parts are on their way at once, the first
+// beside the LSE.  Of nw warps warp w sums parts w, w + nw, ...
 template <int R>
-__global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedArgs a) {
-  grid_dependency_wait();
-  constexpr int kL = (kPgMaxCtas + 31) / 32;
-  const int lane = threadIdx.x & 31;
-  const int work = a.joins[0].x * R;
-  for (int x = (blockIdx.x * kPgJoinThreads + threadIdx.x) >> 5; x < work;
-       x += gridDim.x * (kPgJoinThreads / 32)) {
-    const int4 jn = a.joins[1 + 2 * (x / R)], jg = a.joins[2 + 2 * (x / R)];
-    const int r = x % R, n = jn.w;
-    if (r >= jg.y) continue;
+struct PgJoin {
+  static constexpr int kL = (kPgMaxCtas + 31) / 32, kAhead = 2;
+  float4 o[4];
+  float mx, l;
+  int h;
+  int64_t orow;  // the row of the output
+  __device__ __forceinline__ PgJoin(const PagedArgs &a, const int4 &jn, const int4 &jg, int r, int w,
+                                    int nw, int lane) {
+    const int n = jn.w;
     // part 0 is CTA jn.z's second, part i the first of CTA jn.z + i
     auto at = [&](int i) { return (int64_t)(2 * (jn.z + i) + (i == 0 ? 1 : 0)) * R + r; };
-    float4 v[kPgAhead][4];
+    float4 v[kAhead][4];
     auto fetch = [&](int i, float4 *d) {
       const float4 *src = reinterpret_cast<const float4 *>(a.o_part + at(i) * CPMLA_DV) + lane;
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[k] = __ldcg(src + 32 * k);
     };
 #pragma unroll
-    for (int i = 0; i < kPgAhead; ++i) fetch(i < n ? i : n - 1, v[i]);
-    const int i = jg.x + r / a.hc, h = jn.y * a.hc + r % a.hc;
-    const int64_t tok = a.tokens ? a.tokens[i] : i;
-    float p[kL], mx = -INFINITY, l = 0.f;
+    for (int i = 0; i < kAhead; ++i) fetch(min(w + nw * i, n - 1), v[i]);
+    const int e = jg.x + r / a.hc;
+    h = jn.y * a.hc + r % a.hc;
+    orow = (int64_t)(a.tokens ? a.tokens[e] : e) * a.H + h;
+    float p[kL];
+    mx = -INFINITY;
+    l = 0.f;
 #pragma unroll
     for (int k = 0; k < kL; ++k) {
       p[k] = lane + 32 * k < n ? __ldcg(a.lse_part + at(lane + 32 * k)) : -INFINITY;
@@ -1151,13 +1179,12 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    float4 o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += kPgAhead) {
+    for (int i0 = w; i0 < n; i0 += nw * kAhead) {
 #pragma unroll
-      for (int y = 0; y < kPgAhead; ++y) {
-        const int ii = i0 + y;
+      for (int u = 0; u < kAhead; ++u) {
+        const int ii = i0 + nw * u;
         float wt = p[0];
 #pragma unroll
         for (int k = 1; k < kL; ++k) wt = ii >> 5 == k ? p[k] : wt;
@@ -1165,23 +1192,64 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
         if (ii >= n) wt = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          o[k].x = fmaf(wt, v[y][k].x, o[k].x);
-          o[k].y = fmaf(wt, v[y][k].y, o[k].y);
-          o[k].z = fmaf(wt, v[y][k].z, o[k].z);
-          o[k].w = fmaf(wt, v[y][k].w, o[k].w);
+          o[k].x = fmaf(wt, v[u][k].x, o[k].x);
+          o[k].y = fmaf(wt, v[u][k].y, o[k].y);
+          o[k].z = fmaf(wt, v[u][k].z, o[k].z);
+          o[k].w = fmaf(wt, v[u][k].w, o[k].w);
         }
-        if (ii + kPgAhead < n) fetch(ii + kPgAhead, v[y]);
+        if (ii + nw * kAhead < n) fetch(ii + nw * kAhead, v[u]);
       }
     }
+  }
+  // Factor of the row's output; the first thread writes L.
+  __device__ __forceinline__ float finish(const PagedArgs &a, bool first) const {
     const bool empty = mx == -INFINITY && l == 0.f;  // l may be NaN
     const float L = empty ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
-    const float f = empty ? 0.f : sink_factor(a.sink, h, L) / l;
-    uint2 *dst = reinterpret_cast<uint2 *>(a.o + (tok * a.H + h) * CPMLA_DV) + lane;
+    if (first) a.lse[orow] = L;
+    return empty ? 0.f : sink_factor(a.sink, h, L) / l;
+  }
+};
+__device__ __forceinline__ uint2 pack_bf16x4(float4 v, float f) {
+  return make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+}
+
+// Every row of every group in the plan's joins: by a warp, or, of more than kPgLongJoin
+// parts, by a CTA.  (One token of 131,072 keys has 152 parts: 39 us a call instead of
+// 78 with a warp for each row.)
+constexpr int kPgJoinThreads = 256, kPgJoinCtas = 152 * 8;
+template <int R>
+__global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedArgs a) {
+  constexpr int kWarps = kPgJoinThreads / 32;
+  __shared__ float4 s_o[kWarps][CPMLA_DV / 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  const int4 counts = a.joins[0];
+  const int n_long = counts.y * R * kWarps;  // one code for both: it comes from L2
+  for (int x = blockIdx.x * kWarps + warp; x < n_long + counts.x * R; x += gridDim.x * kWarps) {
+    const bool lng = x < n_long;  // of all of the CTA's warps
+    const int y = lng ? x / kWarps : x - n_long, r = y % R;
+    const int k = lng ? kPgMaxCtas - 1 - y / R : y / R;
+    const int4 jn = a.joins[1 + 2 * k], jg = a.joins[2 + 2 * k];
+    if (r >= jg.y) continue;
+    PgJoin<R> j(a, jn, jg, r, lng ? warp : 0, lng ? kWarps : 1, lane);
+    int c = lane;  // channels 4 c .., and three times 128 further
+    if (lng) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      dst[32 * k] = make_uint2(pack_bf16x2(o[k].x * f, o[k].y * f),
-                               pack_bf16x2(o[k].z * f, o[k].w * f));
-    if (lane == 0) a.lse[tok * a.H + h] = L;
+      for (int i = 0; i < 4; ++i) s_o[warp][32 * i + lane] = j.o[i];
+      __syncthreads();
+      c = threadIdx.x % (CPMLA_DV / 4);
+      j.o[0] = s_o[0][c];
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 v = s_o[w][c];
+        j.o[0] = make_float4(j.o[0].x + v.x, j.o[0].y + v.y, j.o[0].z + v.z, j.o[0].w + v.w);
+      }
+      __syncthreads();
+    }
+    const float f = j.finish(a, lane == 0);
+    uint2 *dst = reinterpret_cast<uint2 *>(a.o + j.orow * CPMLA_DV) + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i == 0 || !lng) dst[32 * i] = pack_bf16x4(j.o[i], f);
   }
 }
 
@@ -1200,28 +1268,32 @@ PgLayout pg_layout(int n, int R) {
   return L;
 }
 
-// Rows per CTA.
+// Rows of a piece: 16 for single tokens of up to 16 heads, else 64.  The lengths lie
+// on the device, so single tokens are told from the list's length and the table's
+// (and an eighth more, for padding and the odd longer one).  Measured, 32 requests of
+// 16,384 keys and 16 heads: with one token each 80 us in 16 rows and 91 in 64 (of
+// which 16 are used), with two 132 and 94; a prompt of 4,096 tokens 1,402 and 410.
+// 32 rows were never the best: 99, 101 and 890 us, and 101 for single tokens of 32
+// heads, 95 in 64 rows.
 int pg_rows(int hc, int n_tokens, int B) {
-  if (n_tokens >= 2 * (int64_t)B || hc > 32) return 64;
-  return hc <= 16 ? 16 : 32;
+  return hc <= 16 && n_tokens <= B + (int64_t)B / 8 ? 16 : 64;
 }
 
 // SMs of the current device (-1 on failure), with the attention's kernel for R
 // rows allowed its shared memory there; asked once a device and R.
 int pg_device(int R) {
   constexpr int kMax = 64;
-  static std::atomic<int> known[3][kMax];
+  static std::atomic<int> known[2][kMax];
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   const bool keep = e == cudaSuccess && dev >= 0 && dev < kMax;
-  std::atomic<int> &slot = known[R == 64 ? 2 : (R == 32 ? 1 : 0)][keep ? dev : 0];
+  std::atomic<int> &slot = known[R == 64 ? 1 : 0][keep ? dev : 0];
   if (keep && (sms = slot.load(std::memory_order_acquire)) > 0) return sms;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if (e == cudaSuccess)
-    e = R == 64   ? cudaFuncSetAttribute(paged_attn_kernel<64>, attr, pg_smem<64>())
-        : R == 32 ? cudaFuncSetAttribute(paged_attn_kernel<32>, attr, pg_smem<32>())
-                  : cudaFuncSetAttribute(paged_attn_kernel<16>, attr, pg_smem<16>());
+    e = R == 64 ? cudaFuncSetAttribute(paged_attn_kernel<64>, attr, pg_smem<64>())
+                : cudaFuncSetAttribute(paged_attn_kernel<16>, attr, pg_smem<16>());
   if (e != cudaSuccess) {
     cuda_fail(e, "mla_paged_attn: device");
     return -1;
@@ -1367,7 +1439,5 @@ extern "C" int mla_paged_attn(const void *q, int64_t q_token_stride, int H, cons
       return fail(CPMLA_ERR_CUDA, "%s: tensor map encode failed (%d)", fn, (int)cr);
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return R == 64   ? launch_paged<64>(a, tm[0], tm[1], st)
-         : R == 32 ? launch_paged<32>(a, tm[0], tm[1], st)
-                   : launch_paged<16>(a, tm[0], tm[1], st);
+  return R == 64 ? launch_paged<64>(a, tm[0], tm[1], st) : launch_paged<16>(a, tm[0], tm[1], st);
 }

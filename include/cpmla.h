@@ -462,7 +462,8 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  *   cache      uint8 [n_blocks, block_size, 576]: E4M3 codes of a token's 512
  *              latent and 64 rope channels
  *   cache_exp  uint8 [n_blocks]: the block's exponent e, stored as e + 127;
- *              every value of the block is code * 2^e
+ *              every value of the block is code * 2^e.  63 .. 247 (e = -64 ..
+ *              120); other bytes are read as the nearest of these
  *   block_table  int32 [B, table_stride]: block of request b's positions
  *              block_size * i .. block_size * i + block_size - 1 at [b, i]
  *   slot       block * block_size + position % block_size
@@ -526,10 +527,11 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  * of o_out / lse_out that no entry names are left as they were.  What lies in
  * the cache at positions a row does not attend to (NaN codes included) does
  * not reach it.
- *   q, q_token_stride, H  as in section 2 (H > 64: a multiple of 64)
+ *   q, q_token_stride, H  as in section 2 (H 1..64 or 128)
  *   block_table      int32 [B, table_stride]; B, table_stride (host)
  *   tokens, pos, req  int32 [n_tokens]; entries of one request side by side
- *                    share its keys' loads (any order is right)
+ *                    share its keys' loads (any order is right); two entries
+ *                    do not name one token (they would race for its row)
  *   n_tokens         (host) >= 0; 0 is a no-op
  *   softmax_scale, sink, T, o_out, lse_out  as in section 2e
  *   workspace        device scratch of mla_paged_attn_workspace_size(H,

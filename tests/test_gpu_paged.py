@@ -426,6 +426,35 @@ def test_attn_blocks_of_very_different_scales():
     check_attn(d, q, o, lse)
 
 
+def test_attn_exponents_outside_their_range():
+    """Bytes of cache_exp outside 63 .. 247 are read as the nearest of these."""
+    b = pu.Batch([70, 300], [1, 1], 32, seed=71)
+    d = b.gpu()
+    d["cache_exp"] = torch.where(d["cache_exp"] % 2 == 0, 0, 62).to(torch.uint8)
+    q = gpu(make_q(2, 16, 72))
+    outs = []
+    for e in (d["cache_exp"], torch.full_like(d["cache_exp"], 63)):
+        outs.append(run_attn(dict(d, cache_exp=e), q))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    d["cache"] = d["cache"] & 0x87  # small codes: 448 x 2^120 would leave binary32
+    outs = []
+    for e in (255, 247):
+        outs.append(run_attn(dict(d, cache_exp=torch.full_like(d["cache_exp"], e)), q,
+                             scale=SCALE * 2.0 ** -120))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    assert all(x.isfinite().all() for x in outs[0]) and cpmla.device_status() == 0
+
+
+@pytest.mark.parametrize("parts_of", [8191, 40000, 300001])
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_attn_one_token_in_many_parts(H, parts_of):
+    """Single tokens whose keys are spread over all SMs, and one of few keys."""
+    b = pu.Batch([parts_of, 33], [1, 1], 64, seed=parts_of)
+    d, q = b.gpu(), gpu(make_q(2, H, 73))
+    o, lse = run_attn(d, q)
+    check_attn(d, q, o, lse)
+
+
 def test_attn_q_range():
     """Channels of q that differ by 2^20, zero rows, and rows of other sizes."""
     b = pu.Batch([300] * 4, [1] * 4, 64, seed=14)
