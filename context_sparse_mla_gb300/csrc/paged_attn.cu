@@ -45,14 +45,14 @@
 // in.  Every wait is bounded; on expiry the CTA records CPMLA_ERR_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and exits.
 //
-// What bounds it, measured.  R = 16 (32 requests of 65,536 keys x 16 heads): HBM;
-// 224 us a call, 5.1 TB/s over the whole call, 5.6 in the kernel.  R = 64: shared
+// What bounds it, measured.  R = 16 (32 tokens of 4,096 to 131,072 keys x 16 heads):
+// HBM; 219 us a call, 5.2 TB/s over the whole call, 5.6 in the kernel.  R = 64: shared
 // memory and the MMA issue.  A tile's 42 MMAs read 188 KB of it (each part of p
 // reads the 4 KB of keys again: three parts side by side would need 768 TMEM
 // columns) and the copies write 36 KB, about 1,800 cycles at 128 B a cycle; it
 // takes 2,050.  Between two pieces the tensor core stands still for about 8 tiles:
 // the last softmax and PV, the output, and q's split do not overlap the next
-// piece's.  8,192 tokens x 16 heads 1,160 us (1.00 PFLOP/s of the exact products).
+// piece's.  8,192 tokens x 16 heads 1,160 us (1.01 PFLOP/s of the exact products).
 #include <atomic>
 #include <cmath>
 #include <cstring>
