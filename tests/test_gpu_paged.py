@@ -203,6 +203,34 @@ def test_insert_same_slot_twice_keeps_the_last(n, bs):
     check_insert(tokens(n, n), slot, cache, torch.full((3,), 118, dtype=torch.uint8), bs)
 
 
+@pytest.mark.parametrize("n", [300, 2500, 5000, 11000])
+@pytest.mark.parametrize("bs", [16, 64, 128])
+def test_insert_runs_of_all_lengths(n, bs):
+    """Single tokens, parts of blocks, whole ones, skipped entries and blocks named
+    more often than they have rows (runs past any window of the list)."""
+    g = np.random.default_rng(n + bs)
+    blocks = iter(g.permutation(n))
+    slot = []
+    while len(slot) < n:
+        b, kind = next(blocks), g.integers(0, 5)
+        if kind == 0:
+            slot.append(b * bs + g.integers(0, bs))
+        elif kind == 1:
+            slot += [-1] * int(g.integers(1, 4))
+        elif kind == 4 and len(slot) > 100:
+            slot += (b * bs + g.integers(0, bs, int(g.integers(200, 700)))).tolist()
+        else:
+            at, k = int(g.integers(0, bs)), int(g.integers(2, bs + 1))
+            slot += [b * bs + x for x in range(at, min(bs, at + k))]
+    slot = np.array(slot[:n])
+    used, at = np.unique(slot[slot >= 0] // bs, return_inverse=True)  # as few blocks as needed
+    slot[slot >= 0] = at * bs + slot[slot >= 0] % bs
+    cache = torch.randint(0, 127, (len(used) + 1, bs, 576), dtype=torch.uint8,
+                          generator=torch.Generator().manual_seed(n))
+    exp = torch.full((len(used) + 1,), 117, dtype=torch.uint8)
+    check_insert(tokens(n, n), slot, cache, exp, bs)
+
+
 def test_insert_skips_and_records_slots_outside():
     bs, cache = 64, torch.zeros((4, 64, 576), dtype=torch.uint8)
     exp = torch.full((4,), 120, dtype=torch.uint8)
@@ -637,3 +665,115 @@ def test_two_graphs_share_one_workspace_in_order():
     for _, d, q, o, lse, o0, l0 in runs:
         assert torch.equal(o, o0) and torch.equal(lse, l0)
         check_attn(d, q, o, lse)
+
+
+# ----------------------------------------------- calls at the edges of what is allowed
+@pytest.mark.parametrize("H", [16, 64])
+def test_attn_far_blocks(H):
+    """Blocks whose bytes lie past 32 bits, and rows of q and o past them too."""
+    b = pu.Batch([70, 300], [1, 3], 64, seed=81)
+    d = b.gpu()
+    n_blocks = (5 << 30) // (64 * 576)
+    cache = torch.zeros((n_blocks, 64, 576), dtype=torch.uint8, device="cuda")
+    exp = torch.zeros(n_blocks, dtype=torch.uint8, device="cuda")
+    cache[-b.n_blocks:], exp[-b.n_blocks:] = d["cache"], d["cache_exp"]
+    table = torch.where(d["block_table"] >= 0, d["block_table"] + (n_blocks - b.n_blocks), -1)
+    T = (1 << 31) // (H * 576) + 5
+    q = torch.zeros((T, H, 576), dtype=torch.bfloat16, device="cuda")
+    q[-4:] = gpu(make_q(4, H, 82))
+    o = torch.zeros((T, H, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((T, H), device="cuda")
+    tok = np.arange(T - 4, T, dtype=np.int32)
+    cpmla.mla_paged_attn(q, cache, exp, table, d["pos"], d["req"], o, lse, softmax_scale=SCALE,
+                         workspace=cpmla.paged_attn_workspace(H, 4), tokens=gpu(tok))
+    torch.cuda.synchronize()
+    check_attn(d, q[-4:], o[-4:], lse[-4:])
+    assert int(o[:-4].count_nonzero()) == 0
+
+
+def test_calls_with_nothing_to_do():
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    out = cpmla.mla_paged_maps(z(2), z(2), z(0), table, block_size=16, n_blocks=4, n_slots=0)
+    assert out["cu_seqlens"].tolist() == [0, 0, 0] and out["free_head"].item() == 0
+    cache, exp = z(4, 16, 576, dt=torch.uint8), z(4, dt=torch.uint8)
+    cpmla.mla_paged_cache_insert(z(0, 576, dt=torch.bfloat16), z(0, dt=torch.int64), cache, exp)
+    cpmla.mla_paged_cache_insert(z(300, 576, dt=torch.bfloat16),
+                                 torch.full((300,), -1, device="cuda"), cache, exp)
+    q = z(5, 16, 576, dt=torch.bfloat16)
+    o, lse = torch.full((5, 16, 512), 7, dtype=torch.bfloat16, device="cuda"), z(5, 16).float()
+    ws = cpmla.paged_attn_workspace(16, 2000)
+    for n in (0, 1, 5, 2000):  # lists of padding only
+        idle = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+        cpmla.mla_paged_attn(q, cache, exp, table, idle, idle, o, lse, softmax_scale=SCALE,
+                             workspace=ws, tokens=z(n))
+    torch.cuda.synchronize()
+    assert (o == 7).all() and (lse == 0).all() and int(exp.max()) == 0
+    assert cpmla.device_status() == 0
+
+
+def test_attn_prompt_in_a_table_of_many_rows():
+    """A prompt shorter than the table is long takes the rows made for single tokens."""
+    new = [0] * 50
+    new[17] = 41
+    b = pu.Batch([100] * 50, new, 32, seed=83)
+    d, q = b.gpu(), gpu(make_q(41, 4, 84))
+    o, lse = run_attn(d, q)
+    check_attn(d, q, o, lse)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_attn_q_that_is_not_finite(H):
+    """A row of q with an infinite or NaN channel is NaN, and no other row."""
+    b = pu.Batch([90, 700], [1, 5], 64, seed=85)
+    d, q = b.gpu(), make_q(6, H, 86)
+    bad = [(0, 3, 5, float("nan")), (2, 0, 575, float("inf")), (5, H - 1, 100, -float("inf"))]
+    for t, h, c, v in bad:
+        q[t, h, c] = v
+    q = gpu(q)
+    o, lse = run_attn(d, q)
+    clean = q.clone()
+    for t, h, c, v in bad:
+        assert lse[t, h].isnan() and o[t, h].isnan().all()
+        clean[t, h] = 0
+    o2, lse2 = run_attn(d, clean)
+    for t, h, c, v in bad:
+        o[t, h], lse[t, h] = o2[t, h], lse2[t, h]
+    check_attn(d, clean, o, lse)
+
+
+def test_two_streams_at_once():
+    """Steps of two servers on streams of their own give what each gives alone."""
+    def serve(s, stream, n):
+        for k in range(n):
+            s.step(stream=stream)
+            with torch.cuda.stream(stream):
+                s.head.copy_(s.maps["free_head"])
+                s.ctx.add_(s.new)
+
+    def fresh(seed):
+        s = Server(3, 16, 32, 90, 300, 8, seed)
+        s.ctx.fill_(0)
+        s.new.copy_(torch.tensor([1, 2, 1]))
+        s.kv.copy_(tokens(8, seed, spread=1))
+        s.q.copy_(make_q(8, 16, seed))
+        return s
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    alone = []
+    for i in range(2):
+        s = fresh(90 + i)
+        torch.cuda.synchronize()
+        serve(s, streams[i], 40)
+        torch.cuda.synchronize()
+        alone.append(s)
+    both = [fresh(90 + i) for i in range(2)]
+    torch.cuda.synchronize()
+    for k in range(40):
+        for i in range(2):
+            serve(both[i], streams[i], 1)
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        for name in ("o", "lse", "cache", "exp", "table", "ctx"):
+            assert torch.equal(getattr(x, name)[:4], getattr(y, name)[:4]), name
+    assert cpmla.device_status() == 0
