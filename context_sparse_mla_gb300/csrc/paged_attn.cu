@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // that runs once a piece took 8 cycles an instruction.
     if (lane == 0) {
       const int me = warp - 1;
-      constexpr int W = Cfg::kWide, rest = kPgParts % W;  // parts a MMA, and in the last
+      constexpr int W = Cfg::kWide;  // parts a MMA
+      static_assert(kPgParts % W == 0, "no part is left over");
       constexpr uint32_t id = idesc_e4m3_e5m2(128, R * W, 1, 0);
-      constexpr uint32_t id_rest = idesc_e4m3_e5m2(128, R * (rest ? rest : W), 1, 0);
       const uint64_t dp = smem_desc(smem_u32(sP), 16, 512, kSwz64);
       const uint64_t dr = smem_desc(smem_u32(sRing), kPgSlot, 1024, kSwz128);
       bool ok = true;
@@ -562,8 +562,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
               for (uint32_t y = 0; y < kPgParts; y += W) {
                 mma_f8_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4),
-                          dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4), y + W <= kPgParts ? id : id_rest,
-                          acc);
+                          dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4), id, acc);
                 acc = 1;
               }
           }
@@ -607,7 +606,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int np = __popc(__ballot_sync(0xffffffffu, kd == 0 && y >= 0));
         const uint32_t slot = j % NS;
         uint64_t *fb = &c.full[slot];
-        uint8_t *dst = sRing + slot * kPgTileBytes + kd * kPgSlot + pg * rows * (kd == 4 ? 64 : 128);
+        uint8_t *dst =
+            sRing + slot * kPgTileBytes + kd * kPgSlot + pg * rows * (kd == 4 ? 64 : 128);
         bool good = true;
         if (lane == 0) {
           good = j < NS || mbar_wait(&c.empty[slot], (j / NS - 1) & 1, abort, a.status);
@@ -735,8 +735,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               for (int k = q4; k < kPgTile; k += R / 16) {
                 const uint32_t nk = __shfl_sync(0xffffffffu, nan, (k >> 5) * 16);
                 if (((nk >> (k & 31)) & 1) == 0) continue;
-                uint4 *kr = reinterpret_cast<uint4 *>(
-                    sRing + jj % NS * kPgTileBytes + (lane >> 3) * kPgSlot + k * 128 + (lane & 7) * 16);
+                uint4 *kr = reinterpret_cast<uint4 *>(sRing + jj % NS * kPgTileBytes +
+                                                      (lane >> 3) * kPgSlot + k * 128 +
+                                                      (lane & 7) * 16);
                 const uint4 v = *kr;
                 auto has = [](uint32_t u) {
                   const uint32_t z = ~u & 0x7F7F7F7Fu;  // a zero byte: a NaN code
@@ -1146,8 +1147,8 @@ struct PgJoin {
   float mx, l;
   int h;
   int64_t orow;  // the row of the output
-  __device__ __forceinline__ PgJoin(const PagedArgs &a, const int4 &jn, const int4 &jg, int r, int w,
-                                    int nw, int lane) {
+  __device__ __forceinline__ PgJoin(const PagedArgs &a, const int4 &jn, const int4 &jg, int r,
+                                    int w, int nw, int lane) {
     const int n = jn.w;
     // part 0 is CTA jn.z's second, part i the first of CTA jn.z + i
     auto at = [&](int i) { return (int64_t)(2 * (jn.z + i) + (i == 0 ? 1 : 0)) * R + r; };
