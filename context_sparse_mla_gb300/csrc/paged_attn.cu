@@ -50,9 +50,9 @@
 // memory and the MMA issue.  A tile's 42 MMAs read 188 KB of it (each part of p
 // reads the 4 KB of keys again: three parts side by side would need 768 TMEM
 // columns) and the copies write 36 KB, about 1,800 cycles at 128 B a cycle; it
-// takes 2,050.  Between two pieces the tensor core stands still for about 8 tiles:
+// takes 2,050.  Between two pieces the tensor core stands still for 10 to 13 tiles:
 // the last softmax and PV, the output, and q's split do not overlap the next
-// piece's.  8,192 tokens x 16 heads 1,160 us (1.01 PFLOP/s of the exact products).
+// piece's.  8,192 tokens x 16 heads 1,155 us (1.01 PFLOP/s of the exact products).
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -109,21 +109,25 @@ struct PgGroup {
   long long u0;                        // tile units before this group
 };
 
+// An entry as it is listed (its loads wait for nothing), and what it says.
+struct PgListed {
+  int b, p, t, lo, hi;
+};
+__device__ __forceinline__ PgListed pg_listed(const PagedArgs &a, int i) {
+  if (i < 0 || i >= a.n) return PgListed{-1, 0, 0, 0, 0};
+  return PgListed{a.req[i], a.pos[i], a.tokens ? a.tokens[i] : i, a.kv_lo ? a.kv_lo[i] : 0,
+                  a.kv_hi ? a.kv_hi[i] : INT32_MAX};
+}
 struct PgEntry {
   bool ok, bad;
   int b, lo, hi;
 };
-__device__ __forceinline__ PgEntry pg_entry(const PagedArgs &a, int i) {
-  PgEntry e{false, false, -1, 1, 0};
-  if (i < 0 || i >= a.n) return e;
-  e.b = a.req[i];
-  if (e.b == -1) return e;
-  const int p = a.pos[i], t = a.tokens ? a.tokens[i] : i;
-  e.bad = e.b < 0 || e.b >= a.B || t < 0 || t >= a.T || p < 0 || p >= (1 << 30) ||
-          (p >> a.shift) >= a.stride;
+__device__ __forceinline__ PgEntry pg_entry(const PagedArgs &a, const PgListed &x) {
+  PgEntry e{false, false, x.b, max(x.lo, 0), min(x.hi, x.p)};
+  if (x.b == -1) return e;
+  e.bad = x.b < 0 || x.b >= a.B || x.t < 0 || x.t >= a.T || x.p < 0 || x.p >= (1 << 30) ||
+          (x.p >> a.shift) >= a.stride;
   e.ok = !e.bad;
-  e.lo = a.kv_lo ? max(a.kv_lo[i], 0) : 0;
-  e.hi = a.kv_hi ? min(a.kv_hi[i], p) : p;
   return e;
 }
 
@@ -153,11 +157,11 @@ __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedA
   const int round = kPgPlanThreads / a.g * a.g;  // entries a round: no group crosses
   long long u_base = 0;
   int n_base = 0;
-  PgEntry nxt = pg_entry(a, tid < round ? tid : -1);
+  PgListed nxt = pg_listed(a, tid < round ? tid : -1);
   for (int r0 = 0; r0 < a.n; r0 += round) {
     const int i = r0 + tid;
-    const PgEntry e = nxt;
-    if (r0 + round < a.n) nxt = pg_entry(a, tid < round ? i + round : -1);
+    const PgEntry e = pg_entry(a, nxt);
+    if (r0 + round < a.n) nxt = pg_listed(a, tid < round ? i + round : -1);
     if (e.bad) record_status(a.status, CPMLA_ERR_INDEX);
     s_b[tid] = e.ok ? e.b : -1;
     s_lo[tid] = e.lo;
@@ -1312,7 +1316,7 @@ int launch_paged(const PagedArgs &a, const CUtensorMap &tm_lat, const CUtensorMa
   // The other two may start while the kernel ahead of them still runs (their setup
   // beside its end) and wait for its end before they read what it wrote.  The
   // attention does so for up to kPgEarly entries: with 2,500 it takes 470 us
-  // instead of 487; with 8,192, where the plan takes 30 us, 1,338 instead of 1,217.
+  // instead of 487; with 8,192, where the plan takes 26 us, 1,338 instead of 1,217.
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;

@@ -14,7 +14,8 @@
 // list entries: one read of the slots around tells all starts and ends.  A run of
 // up to kShortRun tokens -- a decode row -- goes to one warp, longer ones to the
 // CTA, 64 rows (one block, or several of 16 or 32 rows) at a time.  A row costs a
-// warp about 90 instructions: maxima and scaling work on pairs of bf16.
+// warp about 150 instructions in all: maxima and scaling work on pairs of bf16
+// (340 with a comparison, a product and a test for infinities a channel).
 // Measured: 131,072 tokens of one prompt 53 us (4.25 TB/s of bytes it must move)
 // in blocks of 64, 57 us in blocks of 16 or 128; 32 single tokens 2.8 us, 8,192
 // prompt tokens 5 us from L2.  What is left is latency: two CTAs of 8 rows a
