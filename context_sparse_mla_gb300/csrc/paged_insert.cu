@@ -4,7 +4,8 @@
 // For the tokens N that a call puts into a block: e_N = the least e >= -64 with
 // amax(N) <= 448 * 2^e; the block's exponent is e_N if N holds row 0 (the block
 // starts anew), else max(old, e_N); a raised exponent re-codes the rows that
-// stay as E4M3(code * 2^(old - e)).  x * 2^-e is exact in binary32, so every
+// stay as E4M3(code * 2^(old - e)).  x * 2^-e is exact (in bf16 too, but for what
+// rounds to 0), so every
 // code is the E4M3 value nearest to the exact quotient.
 //
 // Bound by HBM: 1152 B read and 576 B written a token, and for few tokens by the
@@ -12,13 +13,16 @@
 // block, so they stay in registers between the maximum and the coding: one read.
 // A CTA takes the runs (tokens of one block, side by side) that start at its
 // list entries: one read of the slots around tells all starts and ends.  A run of
-// up to kShortRun tokens -- a decode row -- goes to one warp, longer ones to the
-// CTA, 64 rows (one block, or several of 16 or 32 rows) at a time.  A row costs a
+// up to kShortRun tokens -- a decode row -- goes to one warp, longer ones, and those
+// that raise their block's scale, to the CTA, 64 rows (one block, or several of 16 or
+// 32 rows) at a time.  A row costs a
 // warp about 150 instructions in all: maxima and scaling work on pairs of bf16
 // (340 with a comparison, a product and a test for infinities a channel).
 // Measured: 131,072 tokens of one prompt 53 us (4.25 TB/s of bytes it must move)
-// in blocks of 64, 57 us in blocks of 16 or 128; 32 single tokens 2.8 us, 8,192
-// prompt tokens 5 us from L2.  What is left is latency: two CTAs of 8 rows a
+// in blocks of 64, 57 us in blocks of 16 or 128; 32 single tokens 2.2 us, 8,192
+// prompt tokens 5.9 us from L2.  Single tokens that all raise their block's scale: 32
+// of them 10 us, 500 16 us (156 and 160 when a warp re-coded its block's rows one after
+// another).  What is left is latency: two CTAs of 8 rows a
 // warp fill an SM's registers (512 threads of 4 rows took 57 us and spilled).
 #include "cpmla_internal.cuh"
 
@@ -140,9 +144,21 @@ __device__ __forceinline__ uint32_t recode(uint32_t w, float f) {
   return e4m3x4(x[0], x[1], x[2], x[3]);
 }
 
-__device__ __noinline__ void recode_row(const PinArgs &a, int64_t slot, float f, int lane) {
-  uint32_t *p = reinterpret_cast<uint32_t *>(a.cache + slot * CPMLA_DQK);
-  for (int i = lane; i < kChunks; i += 32) p[i] = recode(p[i], f);
+// A row's codes, as they lie in the cache, and written back times f.
+__device__ __forceinline__ Row load_codes(const PinArgs &a, int64_t slot, int lane) {
+  Row r;
+  const uint32_t *src = reinterpret_cast<const uint32_t *>(a.cache + slot * CPMLA_DQK) + lane;
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    r.v[i].x = (i < 4 || lane < kChunks - 128) ? src[32 * i] : 0;
+  return r;
+}
+__device__ __forceinline__ void recode_row(const PinArgs &a, int64_t slot, const Row &r, float f,
+                                           int lane) {
+  uint32_t *dst = reinterpret_cast<uint32_t *>(a.cache + slot * CPMLA_DQK) + lane;
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    if (i < 4 || lane < kChunks - 128) dst[32 * i] = recode(r.v[i].x, f);
 }
 
 __device__ __forceinline__ int old_exp(const PinArgs &a, int64_t blk) {
@@ -207,12 +223,15 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
         len += b ? __ffs(b) - 1 : 32;
       } while (b == 0);
     }
-    if (len > kShortRun) {
+    auto leave = [&] {  // to the whole CTA
       if (lane == 0) {
         const int i = atomicAdd(&s_n_long, 1);
         s_start[i] = c;
         s_len[i] = len;
       }
+    };
+    if (len > kShortRun) {
+      leave();
       continue;
     }
     const int eo = old_exp(a, blk);
@@ -252,19 +271,11 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
     }
     int e = exp_of(m);
     if (!starts) {
-      if (eo >= e) {
-        e = eo;
-      } else {
-        const float f = pow2_neg(e - eo);
-        for (int row = 0; row < bs; ++row) {
-          const int64_t sl = (blk << a.shift) + row;
-          bool mine = false;
-#pragma unroll
-          for (int u = 0; u < kShortRun; ++u) mine |= s[u] == sl;
-          if (mine) continue;
-          recode_row(a, sl, f, lane);
-        }
+      if (eo < e) {  // the block's other rows are re-coded
+        leave();
+        continue;
       }
+      e = eo;
     }
     const uint32_t inv = inv_scale(e);
 #pragma unroll
@@ -326,17 +337,25 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
     const uint32_t inv = inv_scale(e);
     // blocks of 128: the registers hold the last 8 rows, the first 8 are read again
     for (int j0 = per - kRowRegs; j0 >= 0 && mine; j0 -= kRowRegs) {
+      if (j0 + kRowRegs < per || f != 1.f) {
+#pragma unroll
+        for (int j = 0; j < kRowRegs; ++j) {
+          const int row = gw + n_warps * (j0 + j), o = owner[row];
+          if (o >= 0) {
+            if (j0 + kRowRegs < per) r[j] = load_row(a, t0 + o, lane);
+          } else if (f != 1.f) {
+            r[j] = load_codes(a, (b << a.shift) + row, lane);
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < kRowRegs; ++j) {
         const int row = gw + n_warps * (j0 + j);
         const int64_t sl = (b << a.shift) + row;
-        const int o = owner[row];
-        if (o >= 0) {
-          if (j0 + kRowRegs < per) r[j] = load_row(a, t0 + o, lane);
+        if (owner[row] >= 0)
           store_row(a, sl, r[j], inv, lane);
-        } else if (f != 1.f) {
-          recode_row(a, sl, f, lane);
-        }
+        else if (f != 1.f)
+          recode_row(a, sl, r[j], f, lane);
       }
     }
     if (mine && gt == 0) a.exp[b] = (uint8_t)(e + 127);
@@ -376,12 +395,13 @@ extern "C" int mla_paged_cache_insert(const void *kv, int64_t kv_token_stride, i
   a.n_slots = (int64_t)n_blocks * block_size;
   a.shift = paged_block_shift(block_size);
   a.status = status;
-  // Entries per CTA: 8, so that 8 decode rows take a warp each, while the CTAs
-  // run at once (two on each of 152 SMs); then more, up to 64, so that a prompt's
-  // long runs need not wait for CTAs that find no start.  Measured with 8, 16,
-  // 32, 64: 500 single tokens 2.9, 4.3, 6.9, 12.3 us; 8,192 prompt tokens 7.9,
-  // 6.4, 5.9, 5.0 us; 131,072 of them 92, 68, 57, 53 us.
-  a.chunk = kPinWarps;
+  // Entries per CTA: one while the CTAs run at once (two on each of 152 SMs), so that
+  // blocks whose scale rises are re-coded side by side (32 single tokens that all
+  // raise theirs take 10 us, 35 with 8 a CTA); then up to 64, so that a prompt's long
+  // runs need not wait for CTAs that find no start.  Measured with 8, 16, 32, 64:
+  // 8,192 prompt tokens 7.9, 6.4, 5.9, 5.0 us; 131,072 of them 92, 68, 57, 53 us; and
+  // the other way 4,000 single tokens 6.9, 8.4, 8.4, 13.4 us.
+  a.chunk = 1;
   while (a.chunk < kMaxChunk && (int64_t)a.chunk * kPinWave < n) a.chunk *= 2;
   const int64_t grid = ((int64_t)n + a.chunk - 1) / a.chunk;
   paged_insert_kernel<<<(unsigned)grid, kPinThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kMapsThreads) paged_maps_kernel(const MapsArgs
     __syncthreads();
     tok0 = s_tok[kMapsThreads];
     blk0 = s_blk[kMapsThreads];
-    // this CTA's entries that belong to this round's requests
+    // this CTA's entries that belong to these requests
     const int64_t lo = s_tok[0] > i0 ? s_tok[0] : i0, hi = tok0 < i1 ? tok0 : i1;
     for (int64_t i = lo + tid; i < hi; i += kMapsThreads) {
       int x = 0, y = kMapsThreads;  // s_tok[x] <= i < s_tok[y]
