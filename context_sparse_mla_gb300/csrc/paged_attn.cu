@@ -13,14 +13,16 @@
 //   * p_j = 2^(u_j - m), as fp16, is the sum of three E5M2: 9 significant bits
 //     (a bf16 has 8) where p >= 2^-8, and at worst 2^-17 off below.  m follows
 //     each tile's maximum both ways: it moves when the tile's largest p leaves
-//     [2^-4, 2^15.75], to make it 2^6, so a weight is off by at most 2^-13 of its
-//     tile's own largest one (2^-23 where m was just set), whatever the other
-//     tiles hold.  (A first token with almost all of the weight and next to no
+//     [2^-4, 2^15.75], so a weight is off by at most 2^-13 of its tile's own
+//     largest one, whatever the other tiles hold.  (A first token with almost all of the weight and next to no
 //     value is common; two E4M3 terms, which need a third fewer MMAs, reach 2^-9
-//     and lose the tokens beside it.)  A move rescales O^T, a few thousand
-//     cycles, hence the wide window: with [2^4, 2^15.75] some CTAs of a 32-row
-//     decode moved 60 times and took 391 us where the others took 235.  m stays
-//     within 2^60 of its highest value, beyond which a tile adds nothing.
+//     and lose the tokens beside it.)  A move rescales O^T and waits
+//     for the PV GEMM before, about a tile's time, hence the wide window, and m goes
+//     no further than it must (p to 2^-2 or 2^14; a row's first to 2^6): the window
+//     comes to lie around the row's tiles.  Scores of standard deviation 4 (32 tokens
+//     of 16,384 keys x 64 heads): 117 us, 138 with every move to 2^6, 97 without moves;
+//     a move at every tile, 197, is the worst.  m stays within 2^60 of its highest
+//     value, beyond which a tile adds nothing.
 // A piece of work is R = 16 or 64 rows (G tokens of one request x Hc heads) and
 // a range of their keys, 64 at a time:
 //   S = [h; l] . C^T      q (2R lanes) in TMEM, the tile's keys as N = 64, K = 576
@@ -790,9 +792,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           m_hi = fmaxf(m_hi, um);
           const float d = um - m_old;  // +inf at a row's first key
           if (d > 15.75f)
-            m_new = um - 6.f;
+            m_new = um - (m_old == -INFINITY ? 6.f : 14.f);
           else if (d < -4.f)
-            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) - 6.f);
+            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) + 2.f);
         }
         if (live && lane < 16) {
           c.m_ref[r] = m_new;
