@@ -21,8 +21,9 @@
 //     no further than it must (p to 2^-2 or 2^14; a row's first to 2^6): the window
 //     comes to lie around the row's tiles.  Scores of standard deviation 4 (32 tokens
 //     of 16,384 keys x 64 heads): 117 us, 138 with every move to 2^6, 97 without moves;
-//     a move at every tile, 197, is the worst.  m stays within 2^60 of its highest
-//     value, beyond which a tile adds nothing.
+//     a move at every tile, 197, is the worst.  How far m may go down is bounded by the
+//     sums that it takes along in binary32 (kPgFallU): a tile further below the row's
+//     largest u adds nothing to O^T.
 // A piece of work is R = 16 or 64 rows (G tokens of one request x Hc heads) and
 // a range of their keys, 64 at a time:
 //   S = [h; l] . C^T      q (2R lanes) in TMEM, the tile's keys as N = 64, K = 576
@@ -366,7 +367,7 @@ struct PgCtrl {
   uint32_t tmem_base;
   int abort;
   float qf[2][R];      // a piece's scale of q row r, times softmax scale and log2 e
-  float m_ref[R], m_hi[R];
+  float m_ref[R], m_low[R];  // the reference, and the least it may become
   float stat_l[2][R];
   alignas(16) float alpha[2][R];
   uint32_t mv[2][4];  // a row quarter has a row whose reference moved
@@ -429,6 +430,18 @@ __device__ __forceinline__ uint2 split_q(uint32_t w, uint32_t down) {
 __device__ __forceinline__ uint2 split_q4(uint32_t w0, uint32_t w1, uint32_t down) {
   const uint2 a = split_q(w0, down), b = split_q(w1, down);
   return make_uint2(a.x | (b.x << 16), a.y | (b.y << 16));
+}
+// How far below the largest u and t = u - e of a row its reference m may lie: two sums
+// over N <= 2^30 keys have to stay in binary32,
+//   O^T  sum 2^(u - m) c   <= N 448 2^(max u - m): 2^117 with m >= max u - 80 + 2
+//   l    sum 2^(u - m - e) <= N 2^(max t - m):     2^124 with m >= max t - 96 + 2
+// (max t is far above max u where the heaviest keys lie in blocks of very small values:
+// one of zeros has e = -64).
+constexpr float kPgFallU = 80.f, kPgFallT = 96.f;
+// x 2^d for d of any size: 2^d itself may lie outside binary32 where the product does not.
+__device__ __forceinline__ float pg_scale(float x, float d) {
+  const float h = fast_exp2(0.5f * d);
+  return x == 0.f ? 0.f : x * h * h;
 }
 // 2^e for the stored exponent e + 127, 63 .. 247
 __device__ __forceinline__ float pg_pow2(int stored) { return __int_as_float(stored << 23); }
@@ -725,7 +738,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         tc_fence_before();
         if (ok) warp_arrive(&c.s_free[wg], lane);
-        float um = -INFINITY, kd[2];  // kd: 2^-e of the thread's two key groups
+        // the row's largest u and t in the tile; 2^-e of the thread's two key groups
+        float um = -INFINITY, tm = -INFINITY, kd[2];
         if (live && ok) {
           if (!open) {
             // NaN codes in a key that not every row may see: weight zero times
@@ -757,15 +771,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             }
           }
           // u = t + e
+          float k0[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float k2 = __shfl_sync(0xffffffffu, kf, (kb >> 4) + g);
-            const float k0 = __shfl_sync(0xffffffffu, ku, (kb >> 4) + g);
+            k0[g] = __shfl_sync(0xffffffffu, ku, (kb >> 4) + g);
             const float f = qf * k2;
             // 2^-e: the exponent field mirrored about that of 1
             kd[g] = __uint_as_float((254u << 23) - __float_as_uint(k2));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(s[16 * g + i], f, k0);
+            for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(s[16 * g + i], f, k0[g]);
           }
           if (!open) {
 #pragma unroll
@@ -776,35 +791,42 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             }
           }
 #pragma unroll
-          for (int n = 0; n < 32; ++n) um = fmaxf(um, s[n]);
+          for (int g = 0; g < 2; ++g) {
+            float ug = s[16 * g];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) ug = fmaxf(ug, s[16 * g + i]);
+            um = fmaxf(um, ug);
+            tm = fmaxf(tm, ug - k0[g]);
+          }
           um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 16));
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
         }
         // the reference follows the tile's maximum when it leaves the window
-        float m_old = -INFINITY, m_hi = -INFINITY;
+        float m_old = -INFINITY, m_low = -INFINITY;
         if (x > w.t0) {
           if (ok) ok = warp_wait(&c.ref[q4], (jj - 1) & 1, lane, abort, a.status);
           if (live) {
             m_old = c.m_ref[r];
-            m_hi = c.m_hi[r];
+            m_low = c.m_low[r];
           }
           __syncwarp();
         }
         float m_new = m_old;
         if (mine && um > -INFINITY) {
-          m_hi = fmaxf(m_hi, um);
+          m_low = fmaxf(m_low, fmaxf(um - kPgFallU, tm - kPgFallT));
           const float d = um - m_old;  // +inf at a row's first key
           if (d > 15.75f)
             m_new = um - (m_old == -INFINITY ? 6.f : 14.f);
           else if (d < -4.f)
-            m_new = fminf(m_old, fmaxf(um, m_hi - 60.f) + 2.f);
+            m_new = fminf(m_old, fmaxf(um, m_low) + 2.f);
         }
         if (live && lane < 16) {
           c.m_ref[r] = m_new;
-          c.m_hi[r] = m_hi;
+          c.m_low[r] = m_low;
         }
         if (ok) warp_arrive(&c.ref[q4], lane);
         if (m_new != m_own) {
-          l = l == 0.f ? 0.f : l * fast_exp2(m_own - m_new);
+          l = pg_scale(l, m_own - m_new);
           m_own = m_new;
         }
         if (x > w.t0 && named_bar_or(bar_wg, 128, m_new != m_old)) {
@@ -903,7 +925,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (live && lane < 16) {
         if (!some && wg == 0) c.m_ref[r] = -INFINITY;
         const float m = some ? c.m_ref[r] : -INFINITY;
-        c.stat_l[wg][r] = l == 0.f ? 0.f : l * fast_exp2(m_own - m);
+        c.stat_l[wg][r] = pg_scale(l, m_own - m);
       }
       named_bar_sync(kBarAll, 256);
       if (ok && some) ok = warp_wait(&c.o_full, piece & 1, lane, abort, a.status);

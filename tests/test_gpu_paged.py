@@ -777,3 +777,54 @@ def test_two_streams_at_once():
         for name in ("o", "lse", "cache", "exp", "table", "ctx"):
             assert torch.equal(getattr(x, name)[:4], getattr(y, name)[:4]), name
     assert cpmla.device_status() == 0
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("cut", [False, True])
+def test_attn_sum_of_zero_blocks_before_far_lower_scores(H, cut):
+    """Blocks of zero tokens (the least exponent, as the insertion gives them), then
+    keys 88 below them, then ordinary ones: 2^-e of a zero block's weights times the
+    way the reference goes down would leave binary32.  Whole, and with the pair of
+    tiles again and again in a row that is cut into parts."""
+    tiles = 400 if cut else 3
+    b = pu.Batch([tiles * 64 - 1], [1], 64, seed=87, spread=1)
+    b.exp[:] = pu.BIAS - 2
+    for i, blk in enumerate(b.table[0, :tiles]):
+        kind = 2 if i == tiles - 1 else i % 2
+        if kind == 0:
+            b.cache[blk], b.exp[blk] = 0, pu.EXP_MIN + pu.BIAS
+        else:  # the last channel is the score: -88 = -352 / 4, and 0
+            b.cache[blk, :, 575] = int(np.flatnonzero(pu.e4m3_values() == -352)[0]) if kind == 1 else 0
+    q = torch.zeros((1, H, 576))
+    q[..., 575] = 24.0
+    d, q, sink = b.gpu(), gpu(q.bfloat16()), gpu(torch.randn(H))
+    o, lse = run_attn(d, q, sink=sink)
+    check_attn(d, q, o, lse, sink=sink)
+    # Without the ordinary keys the output is values below 2^7 (448 / 4) at weights of
+    # e^-88 < 2^-126, less than a normal binary32: 2^-119 in all, or nothing.
+    hi = tiles * 64 - 65
+    ref = pu.attend(q, d["cache"], d["cache_exp"], d["block_table"], [0], b.pos, b.req, SCALE, sink,
+                    hi=[hi])[0]
+    o, lse = run_attn(d, q, sink=sink, hi=[hi])
+    assert ((lse[0].double() - ref[1]).abs() <= LSE_ABS + LSE_REL * ref[1].abs()).all()
+    assert (ref[0].abs() <= 2.0 ** -119).all() and (o.abs() <= 2.0 ** -119).all()
+    assert cpmla.device_status() == 0
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("first", ["zeros", "large"])
+def test_attn_sum_of_blocks_at_both_ends_of_the_exponents(H, first):
+    """Zero tokens (e = -64) beside tokens at e = 120 with scores of the same size:
+    the zero ones have a good part of the weight."""
+    b = pu.Batch([191], [1], 64, seed=88)
+    order = [0, 1, 0] if first == "zeros" else [1, 0, 1]
+    for blk, large in zip(b.table[0], order):
+        if large:  # values below 2^122; the scores lie around -1 .. 1
+            b.cache[blk] = b.cache[blk] & 0x80 | 0x38 + b.cache[blk] % 8
+            b.exp[blk] = 247
+        else:
+            b.cache[blk], b.exp[blk] = 0, 63
+    d, q = b.gpu(), gpu(make_q(1, H, 89))
+    scale = SCALE * 2.0 ** -120
+    o, lse = run_attn(d, q, scale=scale)
+    check_attn(d, q, o, lse, scale=scale)
