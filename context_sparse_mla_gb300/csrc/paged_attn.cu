@@ -679,11 +679,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       const int p = ((w.m.t_lo + y) << kPgTileLog) + (lane & 3) * 16;
       if (y >= w.t1 || p + 15 < w.m.lo_min || p > w.m.hi_max) return -1;
       const int blk = row[p >> a.shift];
-      if (blk < 0 || blk >= a.n_blocks) {
-        record_status(a.status, CPMLA_ERR_INDEX);
-        return -1;
-      }
-      return blk;
+      return blk >= 0 && blk < a.n_blocks ? blk : -1;
     };
     auto exp_of_block = [&](int blk) {
       return blk >= 0 ? max(63, min((int)__ldg(a.exp + blk), 247)) : -1;
@@ -783,6 +779,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(s[16 * g + i], f, k0[g]);
           }
           if (!open) {
+            // a group without a block that the row attends to: its block is a bad one
+            // (between the ranges of two rows of a piece a block may be anything)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int p = p0 + kb + 16 * g;
+              if (((there >> ((kb >> 4) + g)) & 1) == 0 && max(lo, p) <= min(hi, p + 15))
+                record_status(a.status, CPMLA_ERR_INDEX);
+            }
 #pragma unroll
             for (int n = 0; n < 32; ++n) {
               const int p = p0 + kb + n;

@@ -828,3 +828,21 @@ def test_attn_sum_of_blocks_at_both_ends_of_the_exponents(H, first):
     scale = SCALE * 2.0 ** -120
     o, lse = run_attn(d, q, scale=scale)
     check_attn(d, q, o, lse, scale=scale)
+
+
+@pytest.mark.parametrize("H", [4, 16, 64])
+def test_attn_blocks_that_no_row_attends_to_may_be_anything(H):
+    """Two tokens of one request with ranges far apart, and blocks between them that
+    were given back: nothing is recorded.  One position of such a block in a range is."""
+    b = pu.Batch([1000], [2], 32, seed=91)
+    b.table[0, 3:20] = -1
+    b.table[0, 7], b.table[0, 9], b.table[0, 19] = b.n_blocks, -77, 1 << 30
+    d, q = b.gpu(), gpu(make_q(2, H, 92))
+    for lo, hi in (([0, 640], [95, 1001]), ([640, 0], [1001, 95]), ([5, 641], [60, 700]),
+                   ([300, 640], [299, 1001])):
+        o, lse = run_attn(d, q, lo=lo, hi=hi)
+        check_attn(d, q, o, lse, lo=lo, hi=hi)
+    for lo, hi in (([0, 640], [96, 1001]), ([639, 0], [1001, 95])):
+        o, lse = run_attn(d, q, lo=lo, hi=hi)
+        check_attn(d, q, o, lse, lo=lo, hi=hi, status=cpmla.CPMLA_ERR_INDEX)
+        cpmla.device_status(clear=True)
