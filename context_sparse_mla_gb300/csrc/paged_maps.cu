@@ -7,7 +7,9 @@
 // local to a token: its request is found by bisection in the token sums, its
 // block comes from the table (index < h_b) or straight from the free list, so
 // no token waits for a table write, and the token that opens a taken block
-// writes that block's table entry.
+// writes that block's table entry.  A block counts as taken also where the token
+// that opens it has no entry (more tokens than n_slots): the last CTA writes the
+// table entries of those.
 //
 // Bound by latency: the arrays of a decode step are kilobytes.  So one launch,
 // and every CTA computes the sums over the requests itself (1024 lengths per
@@ -120,6 +122,22 @@ __global__ void __launch_bounds__(kMapsThreads) paged_maps_kernel(const MapsArgs
       a.slot[i] = blk < 0 ? -1 : ((int64_t)blk << a.shift) + (p & (bs - 1));
       a.pos[i] = (int32_t)(p < INT32_MAX ? p : INT32_MAX);
       a.req[i] = r0 + x;
+    }
+    // blocks that tokens behind n_slots open: a warp a request
+    if (tok0 > a.n_slots && blockIdx.x == gridDim.x - 1) {
+      for (int x = warp; x < kMapsThreads && r0 + x < a.B; x += kMapsThreads / 32) {
+        if (s_tok[x + 1] <= a.n_slots) continue;
+        const int64_t c = s_ctx[x], held = (c + bs - 1) >> a.shift;
+        // the first column that opens at an entry >= n_slots, and the end of those taken
+        const int64_t from = (c + a.n_slots - s_tok[x] + bs - 1) >> a.shift;
+        const int64_t end = held + s_blk[x + 1] - s_blk[x];
+        const int64_t last = end < a.stride ? end : a.stride;
+        for (int64_t col = (from > held ? from : held) + lane; col < last; col += 32) {
+          const int64_t k = s_blk[x] + col - held;
+          const int blk = k >= 0 && k < a.n_free ? a.free_blocks[k] : -1;
+          a.table[(int64_t)(r0 + x) * a.stride + col] = blk >= 0 && blk < a.n_blocks ? blk : -1;
+        }
+      }
     }
     __syncthreads();  // the sums are read
   }

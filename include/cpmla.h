@@ -494,8 +494,11 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  *                     the same word as free_head)
  * Recorded as CPMLA_ERR_INDEX in the status word, the rest of the batch
  * unaffected: a negative length (taken as 0), more tokens than n_slots (those
- * behind are dropped), a table or free list that is too short, or a block
- * outside [0, n_blocks) in either (the tokens get slot -1).
+ * behind are dropped; their blocks are taken and written to the table all the
+ * same, and cu_seqlens counts them), a table or free list that is too short, or
+ * a block outside [0, n_blocks) in either (the tokens get slot -1, and a table
+ * entry that has no block -1).  free_head_out counts what the lengths ask for,
+ * so blocks beyond the end of a table row or of the free list too.
  *
  * mla_paged_cache_insert -- tokens into their slots.  For a block, let N be
  * the tokens of the call with a slot in it and e_N the least exponent >= -64

@@ -846,3 +846,40 @@ def test_attn_blocks_that_no_row_attends_to_may_be_anything(H):
         o, lse = run_attn(d, q, lo=lo, hi=hi)
         check_attn(d, q, o, lse, lo=lo, hi=hi, status=cpmla.CPMLA_ERR_INDEX)
         cpmla.device_status(clear=True)
+
+
+@pytest.mark.parametrize("bs", [16, 128])
+@pytest.mark.parametrize("ctx, new", [
+    ([20, 5, 0], [30, 40, 10]), ([100, 0], [5000, 3000]), ([7] * 40 + [0], [100] * 40 + [9000]),
+    ([0] * 1500, [33] * 1500),
+])
+def test_maps_blocks_of_tokens_that_are_dropped(bs, ctx, new):
+    """Every block that is counted as taken stands in its request's table, also where
+    its tokens lie behind n_slots."""
+    held = [-(-c // bs) for c in ctx]
+    total = sum(-(-(c + n) // bs) for c, n in zip(ctx, new))
+    perm = np.random.default_rng(bs).permutation(total)
+    table = np.full((len(ctx), max(-(-(c + n) // bs) for c, n in zip(ctx, new)) + 1), -7)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = perm[at:at + h]
+        at += h
+    T = sum(new)
+    cu, slot, pos, req, head, after = pu.maps(ctx, new, perm, at, table, bs, T)
+    for n in sorted({0, 1, new[0] - 1, new[0], new[0] + 1, T // 2, T - new[-1], T - 1}):
+        got, t = run_maps(ctx, new, perm, at, table, bs, total, n)
+        assert cpmla.device_status() == cpmla.CPMLA_ERR_INDEX
+        assert np.array_equal(t, after), n
+        assert got["free_head"][0] == head and np.array_equal(got["cu_seqlens"], cu)
+        for k, w in (("slot_mapping", slot), ("pos", pos), ("req", req)):
+            assert np.array_equal(got[k], w[:n]), (k, n)
+
+
+def test_maps_dropped_tokens_beyond_the_table_and_the_free_list():
+    """... and not beyond either: what is not there is -1 or left out."""
+    table = np.full((2, 4), -7)
+    free = np.arange(3)
+    got, t = run_maps([0, 0], [200, 40], free, 0, table, 16, 50, 20)
+    assert cpmla.device_status() == cpmla.CPMLA_ERR_INDEX
+    assert t.tolist() == [[0, 1, 2, -1], [-1, -1, -1, -7]]
+    assert got["free_head"][0] == 16 and got["slot_mapping"].tolist() == list(range(20))
