@@ -11,19 +11,24 @@
 // Bound by HBM: 1152 B read and 576 B written a token, and for few tokens by the
 // chain slots -> rows -> maximum -> codes.  The scale depends on all tokens of a
 // block, so they stay in registers between the maximum and the coding: one read.
-// A CTA takes the runs (tokens of one block, side by side) that start at its
-// list entries: one read of the slots around tells all starts and ends.  A run of
-// up to kShortRun tokens -- a decode row -- goes to one warp, longer ones, and those
-// that raise their block's scale, to the CTA, 64 rows (one block, or several of 16 or
-// 32 rows) at a time.  A row costs a
-// warp about 150 instructions in all: maxima and scaling work on pairs of bf16
-// (340 with a comparison, a product and a test for infinities a channel).
-// Measured: 131,072 tokens of one prompt 53 us (4.25 TB/s of bytes it must move)
-// in blocks of 64, 57 us in blocks of 16 or 128; 32 single tokens 2.2 us, 8,192
-// prompt tokens 5.9 us from L2.  Single tokens that all raise their block's scale: 32
-// of them 10 us, 500 16 us (156 and 160 when a warp re-coded its block's rows one after
-// another).  What is left is latency: two CTAs of 8 rows a
-// warp fill an SM's registers (512 threads of 4 rows took 57 us and spilled).
+// A CTA takes the runs (tokens of one block, side by side but for skipped entries
+// between them) that start at its list entries: one read of the slots around tells
+// starts and ends, where skipped entries do not fill all of it; then the CTA looks
+// further, 1,024 entries at a time.  A run of up to kShortRun entries -- a decode row --
+// goes to one warp, longer ones, and those that raise their block's scale, to the CTA,
+// 64 rows (one block, or several of 16 or 32 rows) at a time.  A row costs a warp about
+// 150 instructions in all: maxima and scaling work on pairs of bf16 (340 with a
+// comparison, a product and a test for infinities a channel).
+// Measured (a call alone, with the cache cold unless named): 131,072 tokens of one
+// prompt 55 us (4.1 TB/s of bytes it must move) in blocks of 64 or 128, 59 us in blocks
+// of 16; in a graph 32 single tokens 2.8 us, 8,192 prompt tokens 6.3 us from L2.  Single
+// tokens that all raise their block's scale: 32 of them 10 us, 500 18 us (156 and 160
+// when a warp re-coded its block's rows one after another).  32 single tokens before
+// 4,000 skipped entries 6.6 us, before 130,000 61 us: the CTA of the last token looks
+// through them.  Runs that ended at a skipped entry, so that one between two tokens of
+// a block made two runs of it, took 53 us for the prompt and 2.2 us for the 32 tokens.
+// What is left is latency: two CTAs of 8 rows a warp fill an SM's registers (512
+// threads of 4 rows took 57 us and spilled).
 #include "cpmla_internal.cuh"
 
 namespace cpmla {
@@ -177,8 +182,9 @@ __device__ __forceinline__ int64_t slot_of(const PinArgs &a, int64_t i, bool rec
 
 __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs a) {
   __shared__ int64_t s_slot[kPinThreads];  // slots from the entry before the CTA's first
-  __shared__ uint32_t s_brk[kPinWarps];    // bit i: a run ends between s_slot[i] and [i + 1]
-  __shared__ uint32_t s_go[kPinWarps];     // bit c: a run starts at the CTA's entry c
+  __shared__ uint32_t s_val[kPinWarps + 1];  // bit i: s_slot[i] is not skipped
+  __shared__ uint32_t s_new[kPinWarps];      // bit i: ... and a run starts with it
+  __shared__ int s_far, s_stop, s_last;      // entries beyond s_slot, by their place in the list
   __shared__ int s_start[kMaxChunk], s_len[kMaxChunk];  // the long ones among them
   __shared__ int s_owner[128];  // long runs: last token of each row of the block, or -1
   __shared__ int s_n_long;
@@ -188,41 +194,98 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
   const int bs = 1 << a.shift;
 
   // ---- one read of the slots around: they tell where runs start and end
-  s_slot[tid] = slot_of(a, i0 - 1 + tid, tid >= 1 && tid <= a.chunk);
-  if (tid == 0) s_n_long = 0;
-  __syncthreads();
-  {
-    const int64_t x = s_slot[tid], y = tid + 1 < kPinThreads ? s_slot[tid + 1] : x;
-    const bool brk = x < 0 || (x ^ y) >> a.shift != 0;
-    const uint32_t b = __ballot_sync(0xffffffffu, brk);
-    const uint32_t g = __ballot_sync(0xffffffffu, brk && y >= 0 && tid < a.chunk);
-    if (lane == 0) {
-      s_brk[warp] = b;
-      s_go[warp] = g;
-    }
+  const int64_t here = slot_of(a, i0 - 1 + tid, tid >= 1 && tid <= a.chunk);
+  s_slot[tid] = here;
+  const uint32_t val = __ballot_sync(0xffffffffu, here >= 0);
+  if (lane == 0) s_val[warp] = val;
+  if (tid == 0) {
+    s_val[kPinWarps] = 0;
+    s_n_long = 0;
+    s_far = s_last = -1;
+    s_stop = INT32_MAX;
   }
   __syncthreads();
+  // the last entry below k of s_slot that is not skipped, or -1
+  auto valid_below = [&](int k) {
+    int w = k >> 5;
+    uint32_t b = s_val[w] & ((1u << (k & 31)) - 1);
+    while (b == 0 && w > 0) b = s_val[--w];
+    return b ? 32 * w + 31 - __clz(b) : -1;
+  };
+  const uint64_t first = ~0ull >> (64 - a.chunk);  // the CTA's entries
+  auto own_bits = [&](const uint32_t *m) {          // ... bits 1 .. chunk of a mask
+    return (m[0] >> 1 | (uint64_t)m[1] << 31 | (uint64_t)m[2] << 63) & first;
+  };
+  // the block of the last entry before s_slot, where an entry of the CTA needs it
+  int64_t before = -1;
+  if ((s_val[0] & 1) == 0 && i0 > 1 && own_bits(s_val) != 0) {
+    bool hit = false;
+    for (int64_t top = i0 - 2; top >= 0 && !hit; top -= 4 * kPinThreads) {
+      int at = -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = top - tid - u * kPinThreads;
+        if (slot_of(a, i, false) >= 0) at = max(at, (int)i);
+      }
+      if (at >= 0) atomicMax(&s_far, at);
+      hit = __syncthreads_or(at >= 0);
+    }
+    if (hit) before = a.slot[s_far] >> a.shift;
+  }
+  bool starts = false;
+  if (here >= 0 && tid >= 1) {
+    const uint32_t b = val & ((1u << lane) - 1);
+    const int p = b ? tid - lane + 31 - __clz(b) : valid_below(tid - lane);
+    starts = (p >= 0 ? s_slot[p] >> a.shift : before) != here >> a.shift;
+  }
+  {
+    const uint32_t g = __ballot_sync(0xffffffffu, starts);
+    if (lane == 0) s_new[warp] = g;
+  }
+  const bool ends = __syncthreads_or(starts && tid > a.chunk);  // all within s_slot
+  uint64_t go = own_bits(s_new);
+  // the first start above k of s_slot, or kPinThreads
+  auto start_above = [&](int k) {
+    int w = (k + 1) >> 5;
+    uint32_t b = w < kPinWarps ? s_new[w] & ~0u << ((k + 1) & 31) : 0;
+    while (b == 0 && ++w < kPinWarps) b = s_new[w];
+    return b ? 32 * w + __ffs(b) - 1 : kPinThreads;
+  };
+  // where the last run ends, if not within s_slot
+  if (go != 0 && !ends && i0 - 1 + kPinThreads < a.n) {
+    const int64_t blk = s_slot[64 - __clzll(go)] >> a.shift;
+    int last = -1;
+    bool stop = false;
+    for (int64_t top = i0 - 1 + kPinThreads; top < a.n && !stop; top += 4 * kPinThreads) {
+      int64_t x[4];
+      int other = INT32_MAX;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = top + tid + u * kPinThreads;
+        x[u] = slot_of(a, i, false);
+        if (x[u] >= 0 && x[u] >> a.shift != blk) other = min(other, (int)i);
+      }
+      if (other != INT32_MAX) atomicMin(&s_stop, other);
+      stop = __syncthreads_or(other != INT32_MAX);
+      const int end = *(volatile int *)&s_stop;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = top + tid + u * kPinThreads;
+        if (x[u] >= 0 && i < end) last = max(last, (int)i);
+      }
+    }
+    if (last >= 0) atomicMax(&s_last, last);
+    __syncthreads();
+  }
   // the runs in turn to the warps
-  uint64_t go = s_go[0] | (uint64_t)s_go[1] << 32;
   for (int k = 0; go != 0; ++k) {
     const int c = __ffsll(go) - 1;
     go &= go - 1;
     if (k % kPinWarps != warp) continue;
     const int64_t t = i0 + c, blk = s_slot[c + 1] >> a.shift;
-    int len = 0;
-    for (int w = (c + 1) >> 5; w < kPinWarps && len == 0; ++w) {
-      const uint32_t b = s_brk[w] & (w == (c + 1) >> 5 ? ~0u << ((c + 1) & 31) : ~0u);
-      if (b) len = 32 * w + __ffs(b) - 1 - c;
-    }
-    if (len == 0) {  // it ends behind the slots read
-      len = kPinThreads - 1 - c;
-      uint32_t b;
-      do {
-        const int64_t x = slot_of(a, t + len + lane, false);
-        b = ~__ballot_sync(0xffffffffu, x >= 0 && x >> a.shift == blk);
-        len += b ? __ffs(b) - 1 : 32;
-      } while (b == 0);
-    }
+    const int end = start_above(c + 1);
+    int len = valid_below(end) - c;
+    if (end == kPinThreads && s_last >= 0) len = s_last - (int)t + 1;
     auto leave = [&] {  // to the whole CTA
       if (lane == 0) {
         const int i = atomicAdd(&s_n_long, 1);
@@ -242,10 +305,8 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
 #pragma unroll
     for (int u = 0; u < kShortRun; ++u) {
       s[u] = -1;
-      if (u < len) {
-        s[u] = s_slot[c + 1 + u];
-        r[u] = load_row(a, t + u, lane);
-      }
+      if (u < len) s[u] = s_slot[c + 1 + u];
+      if (s[u] >= 0) r[u] = load_row(a, t + u, lane);
     }
     // of tokens with one slot the last is kept
 #pragma unroll
@@ -263,7 +324,7 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
     if (m >= kInfBits) {
       m = 0;
       for (int u = 0; u < len; ++u) {
-        bool kept = true;  // s[u] of the list, without an index known at run time
+        bool kept = s_slot[c + 1 + u] >= 0;  // s[u], without an index known at run time
         for (int w = u + 1; w < len; ++w) kept &= s_slot[c + 1 + w] != s_slot[c + 1 + u];
         if (kept) m = finite_amax(a, t + u, lane, m);
       }
@@ -299,8 +360,8 @@ __global__ void __launch_bounds__(kPinThreads) paged_insert_kernel(const PinArgs
     if (gt == 0) s_amax[g] = 0;
     __syncthreads();
     for (int i = gt; i < L; i += n_warps * 32) {
-      const int64_t x = w + 1 + i < kPinThreads ? s_slot[w + 1 + i] : a.slot[t0 + i];
-      atomicMax(&owner[x & (bs - 1)], i);
+      const int64_t x = w + 1 + i < kPinThreads ? s_slot[w + 1 + i] : slot_of(a, t0 + i, false);
+      if (x >= 0) atomicMax(&owner[x & (bs - 1)], i);
     }
     __syncthreads();
     // row gw + n_warps j of the block is this warp's, 8 of them at once
@@ -399,8 +460,8 @@ extern "C" int mla_paged_cache_insert(const void *kv, int64_t kv_token_stride, i
   // blocks whose scale rises are re-coded side by side (32 single tokens that all
   // raise theirs take 10 us, 35 with 8 a CTA); then up to 64, so that a prompt's long
   // runs need not wait for CTAs that find no start.  Measured with 8, 16, 32, 64:
-  // 8,192 prompt tokens 7.9, 6.4, 5.9, 5.0 us; 131,072 of them 92, 68, 57, 53 us; and
-  // the other way 4,000 single tokens 6.9, 8.4, 8.4, 13.4 us.
+  // 8,192 prompt tokens 9.7, 7.1, 6.2, 5.4 us; 131,072 of them 109, 76, 59, 55 us; and
+  // the other way 4,000 single tokens 6.7, 7.9, 8.3, 14.5 us.
   a.chunk = 1;
   while (a.chunk < kMaxChunk && (int64_t)a.chunk * kPinWave < n) a.chunk *= 2;
   const int64_t grid = ((int64_t)n + a.chunk - 1) / a.chunk;

@@ -513,8 +513,9 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  *                    cache is skipped and recorded as CPMLA_ERR_INDEX
  *   cache, cache_exp  the cache; cache 16-byte aligned
  * The tokens of one block stand next to each other in the list, as
- * mla_paged_maps lists them (those of two separate runs of one block would
- * race for its exponent).  Of tokens with the same slot the last one is kept.
+ * mla_paged_maps lists them; skipped entries may lie between them.  (Two runs of
+ * one block with tokens of another block between them would race for its
+ * exponent.)  Of tokens with the same slot the last one is kept.
  * Blocks that no token has a slot in are not touched.
  *
  * mla_paged_attn -- attention of listed tokens over the cache.  Entry i is

@@ -883,3 +883,69 @@ def test_maps_dropped_tokens_beyond_the_table_and_the_free_list():
     assert cpmla.device_status() == cpmla.CPMLA_ERR_INDEX
     assert t.tolist() == [[0, 1, 2, -1], [-1, -1, -1, -7]]
     assert got["free_head"][0] == 16 and got["slot_mapping"].tolist() == list(range(20))
+
+
+def with_skips(slot, g, gaps):
+    """The list with skipped entries strewn into it."""
+    out = []
+    for s in slot:
+        out.append(s)
+        if g.random() < 0.15:
+            out += [-1] * int(g.choice(gaps))
+    return np.array(out, np.int64)
+
+
+@pytest.mark.parametrize("gaps", [[1, 2, 3], [1, 40, 260], [2500]])
+@pytest.mark.parametrize("bs, ctx, new", [
+    (16, [0], [5]), (64, [64], [3]), (64, [5, 130, 0, 64], [1, 100, 64, 2]),
+    (128, [100, 7], [300, 215]), (16, [3] * 40, [1] * 40), (32, [9], [700]),
+])
+def test_insert_skipped_entries_between_tokens_of_a_block(bs, ctx, new, gaps):
+    """Skipped entries do not part the tokens of a block: one exponent comes from all
+    of them, and rows are re-coded once.  Near, over many entries, and at both ends."""
+    b = pu.Batch(ctx, new, bs, seed=bs + len(gaps))
+    g = np.random.default_rng(bs + len(ctx))
+    slot = b.table[b.req, b.pos // bs].astype(np.int64) * bs + b.pos % bs
+    if gaps == [2500]:
+        slot = slot[:40]
+    slot = with_skips(slot, g, gaps)
+    for x in (slot, np.concatenate([[-1] * gaps[-1] * 2, slot, [-1] * 3000])):
+        check_insert(tokens(len(x), 7), x, b.cache, b.exp, bs)
+
+
+@pytest.mark.parametrize("n", [300, 5000, 20000])
+@pytest.mark.parametrize("bs", [16, 128])
+def test_insert_runs_of_all_lengths_with_skipped_entries(n, bs):
+    """Whole and part blocks, single tokens and blocks named more often than they have
+    rows, with skipped entries in and between them, for every number of entries a CTA."""
+    g = np.random.default_rng(n + bs)
+    slot, b = [], 0
+    while len(slot) < n:
+        at, k = int(g.integers(0, bs)), int(g.integers(1, bs + 1))
+        run = [b * bs + x for x in range(at, min(bs, at + k))]
+        if g.random() < 0.05:
+            run = (b * bs + g.integers(0, bs, 400)).tolist()
+        run = with_skips(run, g, [1, 2, 5, 300]) if g.random() < 0.3 else run
+        slot += list(run) + [-1] * int(g.choice([0, 0, 1, 4]))
+        b += 1
+    slot = np.array(slot[:n], np.int64)
+    cache = torch.randint(0, 127, (b + 1, bs, 576), dtype=torch.uint8,
+                          generator=torch.Generator().manual_seed(n))
+    check_insert(tokens(n, n), slot, cache, torch.full((b + 1,), 117, dtype=torch.uint8), bs)
+
+
+def test_insert_slots_outside_leave_their_neighbours_right():
+    """A slot outside the cache between two tokens of a block is recorded, and the
+    block gets what the others alone would give it."""
+    bs = 64
+    cache = torch.randint(0, 127, (4, bs, 576), dtype=torch.uint8)
+    exp = torch.full((4,), 110, dtype=torch.uint8)
+    slot = np.array([64, 4 * 64, 65, -1, -2, 1 << 40, 66, 130, 1 << 33, 131, 3 * 64 + 5, -9, 3 * 64 + 9])
+    kv = tokens(len(slot), 2)
+    kv[6] *= 16  # the last of a block has the largest values
+    kv[9] *= 16
+    inside = np.where((slot >= 0) & (slot < 4 * bs), slot, -1)
+    want, we = pu.insert(kv.double().numpy(), inside, pu.decode(cache.numpy()), exp.numpy(), bs)
+    got, ge = run_insert(kv, slot, cache, exp)
+    assert cpmla.device_status() == cpmla.CPMLA_ERR_INDEX
+    assert np.array_equal(ge.numpy(), we) and np.array_equal(pu.decode(got.numpy()), want)
