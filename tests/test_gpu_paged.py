@@ -949,3 +949,83 @@ def test_insert_slots_outside_leave_their_neighbours_right():
     got, ge = run_insert(kv, slot, cache, exp)
     assert cpmla.device_status() == cpmla.CPMLA_ERR_INDEX
     assert np.array_equal(ge.numpy(), we) and np.array_equal(pu.decode(got.numpy()), want)
+
+
+def weight_errors(d, q, i, hi, scale=SCALE, tile=64):
+    """For entry i, sum_j |v_j| times what the error of weight j may be, as normalised
+    weights: of itself 2^-9 (nine bits) and 2^-11 (as fp16 before), and of the largest
+    in its tile 2^-13 (2^-17 where the window ends at 2^-4); a twentieth more for the
+    score's and the exponential's own."""
+    bs = d["cache"].shape[1]
+    k = torch.arange(hi + 1, device="cuda")
+    blk = d["block_table"][int(d["req"][i]), k // bs].long()
+    val = torch.from_numpy(pu.e4m3_values()).cuda()[d["cache"][blk, k % bs].long()]
+    val = val * torch.exp2(d["cache_exp"][blk].double() - pu.BIAS)[:, None]
+    p = torch.softmax(q[i].double() @ val.T * scale, 1)
+    big = torch.nn.functional.pad(p, (0, -len(k) % tile)).view(len(p), -1, tile).amax(2)
+    err = 1.05 * ((2.0 ** -9 + 2.0 ** -11) * p + 2.0 ** -13 * big[:, k // tile])
+    return err @ val[:, :512].abs()
+
+
+@pytest.mark.parametrize("before", [None, 0.0, 6.5, -26.0])
+@pytest.mark.parametrize("T, H", [(1, 16), (1, 64), (8, 16)])
+def test_attn_output_of_keys_beside_one_that_has_the_weight(T, H, before):
+    """A key with nearly all of the weight and no value; the 63 beside it, each with
+    2^-9.4 of its weight, and as many of 2^-10.8, are all that the output consists of.  The
+    key comes first, or behind a tile of keys without value whose scores (before) put
+    the weights at one or the other place of the reference's window."""
+    tiles = 1 if before is None else 2
+    L = tiles * 64
+    b = pu.Batch([L + 64 - T], [T], 64, seed=93, spread=1)
+    b.exp[:] = pu.BIAS - 3  # a code is 8 times its value
+    code = lambda x: int(np.argmin(np.abs(np.nan_to_num(pu.e4m3_values(), nan=1e9) - 8 * x)))
+    at = tiles - 1
+    if before is not None:
+        b.cache[b.table[0, 0]] = 0
+        b.cache[b.table[0, 0], :, 575] = code(before)
+    b.cache[b.table[0, at], :, 575] = code(-6.5)
+    b.cache[b.table[0, at], 17] = 0                   # the key: score 0
+    b.cache[b.table[0, at + 1], :, 575] = code(-7.5)
+    q = torch.zeros((T, H, 576))
+    q[..., 575] = 24.0
+    d, q = b.gpu(), gpu(q.bfloat16())
+    o, lse = run_attn(d, q)
+    ref = pu.attend(q, d["cache"], d["cache_exp"], d["block_table"], np.arange(T), b.pos, b.req,
+                    SCALE)
+    assert cpmla.device_status() == 0
+    for i, (ro, rl, w) in ref.items():
+        assert ((lse[i].double() - rl).abs() <= LSE_ABS + LSE_REL * rl.abs()).all()
+        err = weight_errors(d, q, i, int(b.pos[i]))
+        diff = (o[i].double() - ro).abs()
+        # the output's own rounding is half a bf16 step, 2^-8
+        assert (diff <= 2.0 ** -8 * ro.abs() + err).all(), float((diff / ro.abs()).max())
+        # and where the tile comes first its largest weight is 2^6 above the reference,
+        # so that the smaller ones keep their 9 bits
+        if before is None:
+            assert (diff <= 2.0 ** -8 * ro.abs() + 2.0 ** -8 * w).all()
+
+
+@pytest.mark.parametrize("T, H, reps", [(1, 64, 1), (16, 4, 1), (4, 16, 1), (1, 128, 1),
+                                        (1, 64, 110), (16, 4, 110)])
+def test_attn_rows_whose_references_move_apart(T, H, reps):
+    """64 rows whose scores rise and fall by up to 104 at tiles of their own, so that
+    one, some or all quarters of the rows move at a tile; in parts of four tiles, and
+    (many requests that share the keys) whole."""
+    L = 64 * 40
+    b = pu.Batch([L - T], [T], 64, seed=94, spread=1)
+    b.exp[:] = pu.BIAS - 3
+    b.table = np.repeat(b.table, reps, 0)
+    b.pos, b.req = np.tile(b.pos, reps), np.repeat(np.arange(reps), T).astype(np.int32)
+    g = torch.Generator().manual_seed(95)
+    vals = [-52.0, -30.0, -8.0, 0.0, 0.0, 8.0, 30.0, 52.0]
+    codes = torch.tensor([int(np.argmin(np.abs(np.nan_to_num(pu.e4m3_values(), nan=1e9) - 8 * x)))
+                          for x in vals], dtype=torch.uint8)
+    for i in range(40):  # eight channels of the rope, of one size each in a tile
+        b.cache[int(b.table[0, i]), :, 568:] = codes[torch.randint(0, 8, (8,), generator=g)]
+    q = torch.zeros((T * reps, H, 576))
+    rows = torch.randint(0, 9, (T * reps, H), generator=g)  # a row's channel; 8: none
+    q[..., 568:] = 24.0 * torch.nn.functional.one_hot(rows, 9)[..., :8]
+    q[..., :512] = torch.randn((T * reps, H, 512), generator=g) * 0.125
+    d, q = b.gpu(), gpu(q.bfloat16())
+    o, lse = run_attn(d, q)
+    check_attn(d, q, o, lse)
