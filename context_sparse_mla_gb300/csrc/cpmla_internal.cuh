@@ -122,6 +122,16 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
+// Inclusive sum over a warp's lanes.
+__device__ __forceinline__ int64_t warp_scan_add(int64_t v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += up;
+  }
+  return v;
+}
+
 // --- programmatic launches: the next grid of the stream may be set up from here
 // on; wait until the grid before has ended and its writes are seen
 __device__ __forceinline__ void grid_launch_dependents() {

@@ -137,15 +137,6 @@ __device__ __forceinline__ PgEntry pg_entry(const PagedArgs &a, const PgListed &
 }
 
 // ------------------------------------------------------------------ the plan
-__device__ __forceinline__ long long pg_scan(long long v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += up;
-  }
-  return v;
-}
-
 // Groups are runs of up to g entries of one request, cut at multiples of g.
 // A group's length in tile units is its tiles plus kPgUnitTail for each head
 // group; CTA c starts at unit floor(total c / n).  One CTA: the entries go by in
@@ -198,15 +189,15 @@ __global__ void __launch_bounds__(kPgPlanThreads) paged_plan_kernel(const PagedA
     }
     const long long units = start ? (long long)a.n_hg * (m.n_tiles + kPgUnitTail) : 0;
     const uint32_t starts = __ballot_sync(0xffffffffu, start);
-    const long long su = pg_scan(units, lane);
+    const long long su = warp_scan_add(units, lane);
     if (lane == 31) {
       s_u[warp] = su;
       s_n[warp] = __popc(starts);
     }
     __syncthreads();
     if (warp == 0) {
-      s_u[lane] = pg_scan(s_u[lane], lane);
-      s_n[lane] = (int)pg_scan(s_n[lane], lane);
+      s_u[lane] = warp_scan_add(s_u[lane], lane);
+      s_n[lane] = (int)warp_scan_add(s_n[lane], lane);
     }
     __syncthreads();
     if (start) {

@@ -22,15 +22,6 @@ namespace {
 constexpr int kMapsThreads = 1024;
 constexpr int kMapsTokens = 2048;  // token entries per CTA
 
-__device__ __forceinline__ int64_t warp_scan_add(int64_t v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += up;
-  }
-  return v;
-}
-
 struct MapsArgs {
   const int32_t *ctx, *nw, *free_blocks, *head;
   int32_t *table, *cu, *pos, *req, *head_out;
