@@ -810,10 +810,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         if (mine && um > -INFINITY) {
           m_low = fmaxf(m_low, fmaxf(um - kPgFallU, tm - kPgFallT));
           const float d = um - m_old;  // +inf at a row's first key
-          if (d > 15.75f)
+          if (d > 15.75f) {
             m_new = um - (m_old == -INFINITY ? 6.f : 14.f);
-          else if (d < -4.f)
+            // from 2^25 on the difference is rounded, to 16 too, which p does not hold
+            if (um - m_new > 15.75f) m_new = um;
+          } else if (d < -4.f) {
             m_new = fminf(m_old, fmaxf(um, m_low) + 2.f);
+          }
         }
         if (live && lane < 16) {
           c.m_ref[r] = m_new;

@@ -1029,3 +1029,35 @@ def test_attn_rows_whose_references_move_apart(T, H, reps):
     d, q = b.gpu(), gpu(q.bfloat16())
     o, lse = run_attn(d, q)
     check_attn(d, q, o, lse)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("e", [15, 16, 17, 18, 19, 20, 30])
+def test_attn_scores_whose_binary32_steps_are_wide(H, e):
+    """Scores up to 288 x 2^e, where a step of a binary32 is as wide as the window of
+    the reference: keys with the largest share the weight evenly, in the first tile or
+    behind others."""
+    b = pu.Batch([64 * 3 - 1, 64 * 6 - 1], [1, 1], 64, seed=97, spread=1)
+    b.exp[:] = pu.BIAS + e
+    b.cache[..., 575] = 0                                  # scores 0 ...
+    code = lambda x: int(np.flatnonzero(pu.e4m3_values() == x)[0])
+    for r, n in enumerate((3, 6)):
+        b.cache[int(b.table[r, n - 1]), :, 575] = code(-256)   # ... the last tile's lower
+        for p in [70, 100, 127, 130] + ([200, 201, 300] if r else []):
+            b.cache[int(b.table[r, p // 64]), p % 64, 575] = code(288)
+    q = torch.zeros((2, H, 576))
+    q[..., 575] = 24.0
+    d, q = b.gpu(), gpu(q.bfloat16())
+    for lo in (0, 64):
+        o, lse = run_attn(d, q, lo=[lo, lo])
+        assert o.isfinite().all() and lse.isfinite().all()
+        # the first row is whole; the second is cut, and its parts are joined by their
+        # LSEs, whose own steps are as wide: any average of the keys' values
+        check_attn(dict(d, pos=d["pos"][:1], req=d["req"][:1]), q, o, lse, lo=[lo])
+        rl = torch.full((H,), 288.0 * 2.0 ** e, dtype=torch.float64, device="cuda")
+        assert ((lse[1].double() - rl).abs() <= 2 + LSE_REL * rl).all()
+        k = torch.tensor([70, 100, 127, 130, 200, 201, 300])
+        v = torch.from_numpy(pu.e4m3_values())[b.cache[b.table[1, k // 64], k % 64].long()].cuda()
+        v = v[:, :512] * 2.0 ** e
+        slack = 2.0 ** -8 * v.abs().amax(0)
+        assert (o[1].double() >= v.amin(0) - slack).all() and (o[1].double() <= v.amax(0) + slack).all()
