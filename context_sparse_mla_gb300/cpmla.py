@@ -414,7 +414,7 @@ def mla_paged_cache_insert(kv, slot_mapping, cache, cache_exp, *, stream=None):
     slot_mapping[t] (int64, -1 skips) of the paged 8-bit cache, in place: cache
     uint8 [n_blocks, block_size, 576] of E4M3 codes and cache_exp uint8
     [n_blocks], the exponent (+ 127) of each block's scale.  The tokens of one
-    block stand side by side."""
+    block stand side by side, but for skipped entries between them."""
     dev = _cuda_index(kv, "kv")
     nb, bs, pc, pe = _paged_cache(cache, cache_exp, dev)
     if kv.dtype is not torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != DQK or kv.stride(1) != 1:
@@ -438,7 +438,9 @@ def mla_paged_attn(q, cache, cache_exp, block_table, pos, req, o_out, lse_out, *
     token tokens[i] (i when None) at position pos[i] of request req[i] (int32;
     req -1 stands for no token), causal and within [kv_lo[i], kv_hi[i]] when
     given.  q [T, H, 576] bf16 (tokens may be strided); writes the entries'
-    rows of o_out [T, H, 512] bf16 (sink applied once) and lse_out [T, H]."""
+    rows of o_out [T, H, 512] bf16 (sink applied once) and lse_out [T, H].  With up
+    to 16 heads and at most an eighth more entries than block_table has rows the list
+    is taken for single tokens, which decides its speed, not its results."""
     dev = _cuda_index(q, "q")
     nb, bs, pc, pe = _paged_cache(cache, cache_exp, dev)
     if (q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != DQK or q.stride(2) != 1

@@ -14,14 +14,14 @@
 //     (a bf16 has 8) where p >= 2^-8, and at worst 2^-17 off below.  m follows
 //     each tile's maximum both ways: it moves when the tile's largest p leaves
 //     [2^-4, 2^15.75], so a weight is off by at most 2^-13 of its tile's own
-//     largest one, whatever the other tiles hold.  (A first token with almost all of the weight and next to no
-//     value is common; two E4M3 terms, which need a third fewer MMAs, reach 2^-9
-//     and lose the tokens beside it.)  A move rescales O^T and waits
-//     for the PV GEMM before, about a tile's time, hence the wide window, and m goes
-//     no further than it must (p to 2^-2 or 2^14; a row's first to 2^6): the window
+//     largest one, whatever the other tiles hold.  (A first token with almost all of
+//     the weight and next to no value is common; two E4M3 terms, which need a third
+//     fewer MMAs, reach 2^-9 and lose the tokens beside it.)  A move rescales O^T and
+//     waits for the PV GEMM before, about a tile's time, hence the wide window, and m
+//     goes no further than it must (p to 2^-2 or 2^14; a row's first to 2^6): the window
 //     comes to lie around the row's tiles.  Scores of standard deviation 4 (32 tokens
-//     of 16,384 keys x 64 heads): 117 us, 138 with every move to 2^6, 97 without moves;
-//     a move at every tile, 197, is the worst.  How far m may go down is bounded by the
+//     of 16,384 keys x 64 heads): 116 us, 138 with every move to 2^6, 96 without moves;
+//     a move at every tile, 196, is the worst.  How far m may go down is bounded by the
 //     sums that it takes along in binary32 (kPgFallU): a tile further below the row's
 //     largest u adds nothing to O^T.
 // A piece of work is R = 16 or 64 rows (G tokens of one request x Hc heads) and
@@ -55,7 +55,7 @@
 // columns) and the copies write 36 KB, about 1,800 cycles at 128 B a cycle; it
 // takes 2,050.  Between two pieces the tensor core stands still for 10 to 13 tiles:
 // the last softmax and PV, the output, and q's split do not overlap the next
-// piece's.  8,192 tokens x 16 heads 1,155 us (1.01 PFLOP/s of the exact products).
+// piece's.  8,192 tokens x 16 heads 1,171 us (1.00 PFLOP/s of the exact products).
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -1303,7 +1303,9 @@ PgLayout pg_layout(int n, int R) {
 // 16,384 keys and 16 heads: with one token each 80 us in 16 rows and 91 in 64 (of
 // which 16 are used), with two 132 and 94; a prompt of 4,096 tokens 1,402 and 410.
 // 32 rows were never the best: 99, 101 and 890 us, and 101 for single tokens of 32
-// heads, 95 in 64 rows.
+// heads, 95 in 64 rows.  B is the table's height and not the number of requests that are
+// there: one prompt in a table of as many rows as it has tokens is in 16 rows too (1,000
+// tokens of 16 heads 165 us, 64 in 64 rows; 200 of 8 heads 25 and 44).
 int pg_rows(int hc, int n_tokens, int B) {
   return hc <= 16 && n_tokens <= B + (int64_t)B / 8 ? 16 : 64;
 }

@@ -501,11 +501,14 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  * so blocks beyond the end of a table row or of the free list too.
  *
  * mla_paged_cache_insert -- tokens into their slots.  For a block, let N be
- * the tokens of the call with a slot in it and e_N the least exponent >= -64
+ * the tokens of the call that its slots keep (of tokens with the same slot the
+ * last one; the others count for nothing) and e_N the least exponent >= -64
  * with |x| <= 448 * 2^e_N for every finite channel x of N.  If N holds the
- * block's row 0, the block starts anew and e = e_N; otherwise e = max(old e,
- * e_N), and where that raises e the block's other rows are re-coded as
- * E4M3(code * 2^(old e - e)).  Then every token of N is written as E4M3(x *
+ * block's row 0, the block starts anew and e = e_N (rows that an earlier call
+ * wrote keep their codes and lose their scale, so a block is filled from row 0
+ * up); otherwise e = max(old e, e_N), and where that raises e the block's other
+ * rows are re-coded as E4M3(code * 2^(old e - e)).  Then every token of N is
+ * written as E4M3(x *
  * 2^-e): nearest, ties to even; infinities saturate to +-448, NaN stays NaN.
  *   kv               bf16 [n, 576], rows kv_token_stride elements apart (host,
  *                    >= 576, a multiple of 8); 16-byte aligned
@@ -513,10 +516,12 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  *                    cache is skipped and recorded as CPMLA_ERR_INDEX
  *   cache, cache_exp  the cache; cache 16-byte aligned
  * The tokens of one block stand next to each other in the list, as
- * mla_paged_maps lists them; skipped entries may lie between them.  (Two runs of
- * one block with tokens of another block between them would race for its
- * exponent.)  Of tokens with the same slot the last one is kept.
- * Blocks that no token has a slot in are not touched.
+ * mla_paged_maps lists them; skipped entries may lie between them.  Two runs of
+ * one block with tokens of another block between them race for its exponent, and
+ * nothing records that: rows gathered from several shards (pcp_dualchunk_partition
+ * cuts chunks where no block need end) are put into position order first, which
+ * mla_kv_cache_insert does not ask for.  Blocks that no token has a slot in are
+ * not touched.
  *
  * mla_paged_attn -- attention of listed tokens over the cache.  Entry i is
  * global token g = tokens[i] (i itself when tokens is NULL) at position t =
@@ -532,7 +537,13 @@ int mla_attn_split_kv_noalloc(const void *q, int64_t q_token_stride, int H, int 
  * the cache at positions a row does not attend to (NaN codes included) does
  * not reach it.
  *   q, q_token_stride, H  as in section 2 (H 1..64 or 128)
- *   block_table      int32 [B, table_stride]; B, table_stride (host)
+ *   block_table      int32 [B, table_stride]; B, table_stride (host).  With up to
+ *                    16 heads a list of at most B + B/8 entries is taken for single
+ *                    tokens and runs in pieces of 16 rows, else of 64: results are
+ *                    right either way, but a prompt beside a table with rows for
+ *                    many more requests than there are takes longer (1,000 tokens x
+ *                    16 heads 165 us with 1,024 rows, 64 with 800).  A captured call
+ *                    keeps the choice that it was captured with
  *   tokens, pos, req  int32 [n_tokens]; entries of one request side by side
  *                    share its keys' loads (any order is right); two entries
  *                    do not name one token (they would race for its row)
