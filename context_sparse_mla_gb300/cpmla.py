@@ -20,12 +20,15 @@ LIB_PATH = os.path.join(_HERE, "libcpmla.so")
 CPMLA_OK, CPMLA_ERR_ARG, CPMLA_ERR_CUDA, CPMLA_ERR_UNSUPPORTED = 0, -1, -2, -3
 CPMLA_ERR_TIMEOUT, CPMLA_ERR_INDEX = -4, -5
 CPMLA_KV_BF16, CPMLA_KV_FP8_E4M3_G128 = 0, 1
-DQK, DV = 576, 512
+CPMLA_ROPE_PAIRS, CPMLA_ROPE_HALVES = 0, 1
+DQK, DV, DROPE = 576, 512, 64
+PAGED4_STRIP_BYTES = 5392
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
+_D = ctypes.c_double
 
 _SIGS = {
     "cpmla_last_error": (ctypes.c_char_p, []),
@@ -58,6 +61,13 @@ _SIGS = {
     "mla_paged_attn_workspace_size": (ctypes.c_size_t, [_I, _I]),
     "mla_paged_attn": (_I, [_P, _I64, _I, _P, _P, _I, _I, _P, _I, _I64, _P, _P, _P, _I, _P, _P,
                             _F, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
+    "mla_rope_freqs": (_I, [_D, _D, _I, _D, _D, _P]),
+    "mla_rope": (_I, [_P, _I64, _I64, _I, _P, _I64, _I64, _P, _I64, _P, _I64, _I, _P, _P, _F, _I,
+                      _I, _P]),
+    "mla_paged4_cache_insert": (_I, [_P, _I64, _I, _P, _P, _I, _I, _P]),
+    "mla_paged4_cache_read": (_I, [_P, _I, _I, _P, _I, _P, _I64, _P]),
+    "mla_paged4_attn": (_I, [_P, _I64, _I, _P, _I, _I, _P, _I, _I64, _P, _P, _P, _I, _P, _P, _F,
+                             _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lock = threading.Lock()
@@ -432,6 +442,29 @@ def paged_attn_workspace(H, n_tokens, device="cuda"):
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
 
 
+def _paged_attn_args(q, cache, block_table, pos, req, o_out, lse_out, softmax_scale, workspace,
+                     tokens, sink, kv_lo, kv_hi, dev):
+    """Checked arguments of both paged attentions; ``cache`` has those of the cache."""
+    if (q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != DQK or q.stride(2) != 1
+            or (q.shape[1] != 1 and q.stride(1) != DQK)):
+        raise ValueError("q must be a bfloat16 [T, H, 576] tensor with contiguous tokens")
+    T, H, _ = q.shape
+    n, i32 = pos.numel(), torch.int32
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    if tokens is None and n > T:
+        raise ValueError("%d entries for %d tokens: give their tokens" % (n, T))
+    return (q.data_ptr(), q.stride(0) if T > 1 else H * DQK, H, *cache,
+            _at(block_table, i32, None, dev, "block_table"), block_table.shape[0],
+            block_table.shape[1], _opt_at(tokens, i32, (n,), dev, "tokens"),
+            _at(pos, i32, (n,), dev, "pos"), _at(req, i32, (n,), dev, "req"), n,
+            _opt_at(kv_lo, i32, (n,), dev, "kv_lo"), _opt_at(kv_hi, i32, (n,), dev, "kv_hi"),
+            softmax_scale, _opt_at(sink, torch.float32, (H,), dev, "sink"), T,
+            _at(o_out, torch.bfloat16, (T, H, DV), dev, "o_out"),
+            _at(lse_out, torch.float32, (T, H), dev, "lse_out"),
+            _at(workspace, torch.uint8, None, dev, "workspace"), workspace.numel())
+
+
 def mla_paged_attn(q, cache, cache_exp, block_table, pos, req, o_out, lse_out, *, softmax_scale,
                    workspace, tokens=None, sink=None, kv_lo=None, kv_hi=None, stream=None):
     """Attention of the listed entries over the paged 8-bit cache: entry i is
@@ -443,25 +476,121 @@ def mla_paged_attn(q, cache, cache_exp, block_table, pos, req, o_out, lse_out, *
     is taken for single tokens, which decides its speed, not its results."""
     dev = _cuda_index(q, "q")
     nb, bs, pc, pe = _paged_cache(cache, cache_exp, dev)
-    if (q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != DQK or q.stride(2) != 1
-            or (q.shape[1] != 1 and q.stride(1) != DQK)):
-        raise ValueError("q must be a bfloat16 [T, H, 576] tensor with contiguous tokens")
-    T, H, _ = q.shape
-    n, i32 = pos.numel(), torch.int32
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, width]")
-    if tokens is None and n > T:
-        raise ValueError("%d entries for %d tokens: give their tokens" % (n, T))
-    _launch((_lib or lib()).mla_paged_attn, dev, stream, q.data_ptr(),
-            q.stride(0) if T > 1 else H * DQK, H, pc, pe, nb, bs,
-            _at(block_table, i32, None, dev, "block_table"), block_table.shape[0],
-            block_table.shape[1], _opt_at(tokens, i32, (n,), dev, "tokens"),
-            _at(pos, i32, (n,), dev, "pos"), _at(req, i32, (n,), dev, "req"), n,
-            _opt_at(kv_lo, i32, (n,), dev, "kv_lo"), _opt_at(kv_hi, i32, (n,), dev, "kv_hi"),
-            softmax_scale, _opt_at(sink, torch.float32, (H,), dev, "sink"), T,
-            _at(o_out, torch.bfloat16, (T, H, DV), dev, "o_out"),
-            _at(lse_out, torch.float32, (T, H), dev, "lse_out"),
-            _at(workspace, torch.uint8, None, dev, "workspace"), workspace.numel())
+    _launch((_lib or lib()).mla_paged_attn, dev, stream,
+            *_paged_attn_args(q, (pc, pe, nb, bs), block_table, pos, req, o_out, lse_out,
+                              softmax_scale, workspace, tokens, sink, kv_lo, kv_hi, dev))
+
+
+# ------------------------------------------------------------ rotary positions
+def rope_freqs(base=10000.0, *, factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0):
+    """The 32 frequencies of the 64 rope channels (float64 numpy, radians a
+    position), scaled for contexts ``factor`` times original_len when factor > 1."""
+    f = np.empty(DROPE // 2)
+    _check(lib().mla_rope_freqs(base, factor, original_len, beta_fast, beta_slow, _ptr(f)))
+    return f
+
+
+def _rope_view(t, n, dim, dev, name):
+    if (t.dtype is not torch.bfloat16 or t.dim() != dim or t.shape[0] != n
+            or t.shape[-1] != DROPE or t.stride(-1) != 1 or t.get_device() != dev):
+        raise ValueError("%s must be a bfloat16 [%s64] view of contiguous channels on cuda:%d"
+                         % (name, "%d, " % n if dim == 2 else "%d, H, " % n, dev))
+    # strides of dimensions of one entry are never used, and may be anything
+    return (t.data_ptr(), *(s if d > 1 else DROPE for d, s in zip(t.shape[:-1], t.stride())))
+
+
+def mla_rope(q, pos, inv_freq, *, k=None, q_out=None, k_out=None, amplitude=1.0, interleaved=True,
+             inverse=False, stream=None):
+    """Rotate the rope channels of n entries at positions pos (int32 [n], below 0:
+    nothing written): q bf16 [n, H, 64] (or None) and k bf16 [n, 64] (or None),
+    views of any strides, into q_out and k_out of the same shapes (None: in place).
+    inv_freq: 32 frequencies (rope_freqs); pairs of channels side by side when
+    interleaved, else 32 apart.  Returns (q_out, k_out)."""
+    dev = _cuda_index(pos, "pos")
+    n = pos.numel()
+    f = np.ascontiguousarray(inv_freq, np.float64)
+    if f.shape != (DROPE // 2,):
+        raise ValueError("inv_freq must hold 32 numbers")
+    a, ao, H = (None, 0, 0), (None, 0, 0), 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        a, ao = _rope_view(q, n, 3, dev, "q"), _rope_view(q_out, n, 3, dev, "q_out")
+        H = q.shape[1]
+        if q_out.shape[1] != H:
+            raise ValueError("q_out must have q's %d heads" % H)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    b, bo = (None, 0), (None, 0)
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        b, bo = _rope_view(k, n, 2, dev, "k"), _rope_view(k_out, n, 2, dev, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _launch((_lib or lib()).mla_rope, dev, stream, *a, H, *ao, *b, *bo, n,
+            _at(pos, torch.int32, (n,), dev, "pos"), f.ctypes.data, amplitude,
+            CPMLA_ROPE_PAIRS if interleaved else CPMLA_ROPE_HALVES, 1 if inverse else 0)
+    return q_out, k_out
+
+
+# ------------------------------------------------------- the paged 4-bit cache
+def paged4_cache(n_blocks, block_size, device="cuda"):
+    """A paged 4-bit latent cache of zeros: uint8 [n_blocks, block_size / 16, 5392]."""
+    if block_size not in (16, 32, 64, 128):
+        raise ValueError("block_size must be 16, 32, 64 or 128")
+    return torch.zeros((n_blocks, block_size // 16, PAGED4_STRIP_BYTES), dtype=torch.uint8,
+                       device=device)
+
+
+def _paged4(cache, dev):
+    if cache.dim() != 3 or cache.shape[2] != PAGED4_STRIP_BYTES:
+        raise ValueError("cache must be [n_blocks, block_size / 16, %d]" % PAGED4_STRIP_BYTES)
+    return cache.shape[0], 16 * cache.shape[1], _at(cache, torch.uint8, None, dev, "cache")
+
+
+def _kv_rows(kv, n, dev, name):
+    if (kv.dtype is not torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != DQK or kv.stride(1) != 1
+            or kv.shape[0] != n or kv.get_device() != dev):
+        raise ValueError("%s must be a bfloat16 [%d, 576] tensor with contiguous rows on cuda:%d"
+                         % (name, n, dev))
+    return kv.data_ptr(), kv.stride(0) if n > 1 else DQK
+
+
+def mla_paged4_cache_insert(kv, slot_mapping, cache, *, stream=None):
+    """Write each token's latent KV row (kv [n, 576] bf16) to slot
+    slot_mapping[t] (int64, -1 skips; distinct) of the paged 4-bit cache
+    (paged4_cache), in place: latent channels as E2M1 codes with a scale for every
+    16 of them, rope channels as E4M3 codes, an exponent a token."""
+    dev = _cuda_index(kv, "kv")
+    nb, bs, pc = _paged4(cache, dev)
+    n = slot_mapping.numel()
+    p, st = _kv_rows(kv, n, dev, "kv")
+    _launch((_lib or lib()).mla_paged4_cache_insert, dev, stream, p, st, n,
+            _at(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), pc, nb, bs)
+
+
+def mla_paged4_cache_read(cache, slot_mapping, *, out=None, stream=None):
+    """The values of the listed slots (int64 [n]; -1: zeros) of the paged 4-bit
+    cache as bf16 rows [n, 576] (``out`` if given; its rows may be strided)."""
+    dev = _cuda_index(cache, "cache")
+    nb, bs, pc = _paged4(cache, dev)
+    n = slot_mapping.numel()
+    if out is None:
+        out = torch.empty((n, DQK), dtype=torch.bfloat16, device=cache.device)
+    p, st = _kv_rows(out, n, dev, "out")
+    _launch((_lib or lib()).mla_paged4_cache_read, dev, stream, pc, nb, bs,
+            _at(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, p, st)
+    return out
+
+
+def mla_paged4_attn(q, cache, block_table, pos, req, o_out, lse_out, *, softmax_scale, workspace,
+                    tokens=None, sink=None, kv_lo=None, kv_hi=None, stream=None):
+    """mla_paged_attn over the paged 4-bit cache: the same entries, bounds, sink,
+    workspace (paged_attn_workspace) and outputs."""
+    dev = _cuda_index(q, "q")
+    nb, bs, pc = _paged4(cache, dev)
+    _launch((_lib or lib()).mla_paged4_attn, dev, stream,
+            *_paged_attn_args(q, (pc, nb, bs), block_table, pos, req, o_out, lse_out, softmax_scale,
+                              workspace, tokens, sink, kv_lo, kv_hi, dev))
 
 
 def device_status(clear=True):

@@ -581,6 +581,114 @@ int mla_paged_attn(const void *q, int64_t q_token_stride, int H, const void *cac
                    void *stream);
 
 /* --------------------------------------------------------------------------
+ * 2h. Rotary positions of queries and keys (device; frequencies on the host)
+ *
+ * The 64 rope channels of the 576-wide rows that every attention here reads are
+ * rotated before; the pages give no rotation, so both usual layouts are there.
+ * Entry t < n at position p = pos[t], for each of its H query heads and its key
+ * (64 channels x each): with angle_i = p * inv_freq[i], i = 0 .. 31, and (u, v) =
+ * (x[2i], x[2i+1]) (CPMLA_ROPE_PAIRS) or (x[i], x[i+32]) (CPMLA_ROPE_HALVES)
+ *   (u', v') = amplitude * (u cos - v sin, u sin + v cos)
+ * in binary32, rounded once to bf16, at the same places of the output; inverse
+ * != 0 negates the angles (which is also the gradient of the rotation, or takes
+ * it back).  The angle is exact modulo a turn to 2^-33 turns at every position.
+ *   q, q_out     bf16; entry t's head h at q + t * q_token_stride + h *
+ *                q_head_stride (elements, host), 64 channels side by side; NULL
+ *                with H = 0.  Views into wider rows are usual: the last 64 of a
+ *                projection's head in, channels 512..575 of q out
+ *   H            heads (host), 0 .. 1024
+ *   k, k_out     bf16; entry t's key at k + t * k_token_stride; both or neither.
+ *                An output may be its input (in place); other overlaps race
+ *   pos          int32 [n]; an entry below 0 stands for no token: nothing is
+ *                written for it
+ *   inv_freq     double [32] (host, read during the call), each 0 .. 6
+ *   amplitude    (host) finite; 1, or what a scaled model multiplies cos and sin by
+ *   layout       CPMLA_ROPE_* (host)
+ * Pointers 8-byte aligned, strides multiples of 4 elements, those of outputs at
+ * least 64 (inputs may repeat a row with stride 0).
+ *
+ * mla_rope_freqs (host): inv_freq[i] = f_i = base^(-2i/64) for factor == 1, else
+ * those of the "YaRN" scaling (Peng et al. 2023): with turns(b) = 64
+ * ln(original_len / (2 pi b)) / (2 ln base), lo = max(0, floor(turns(beta_fast))),
+ * hi = min(63, ceil(turns(beta_slow))) and r = clamp((i - lo) / (hi - lo), 0, 1),
+ *   inv_freq[i] = f_i (1 - r) + f_i / factor * r
+ *   base > 1, factor >= 1; original_len >= 1 and 0 < beta_slow < beta_fast when
+ *   factor > 1 (32 and 1 are usual)
+ * Errors: CPMLA_ERR_ARG, CPMLA_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+enum { CPMLA_ROPE_PAIRS = 0, CPMLA_ROPE_HALVES = 1 };
+
+int mla_rope_freqs(double base, double factor, int original_len, double beta_fast,
+                   double beta_slow, double *inv_freq);
+
+int mla_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int H, void *q_out,
+             int64_t qo_token_stride, int64_t qo_head_stride, const void *k, int64_t k_token_stride,
+             void *k_out, int64_t ko_token_stride, int n, const int32_t *pos,
+             const double *inv_freq, float amplitude, int layout, int inverse, void *stream);
+
+/* --------------------------------------------------------------------------
+ * 2i. The paged 4-bit latent cache (device)
+ *
+ * A cache like that of 2g with 337 bytes a token instead of 576, for the block
+ * tables and slots of mla_paged_maps (blocks of 16, 32, 64 or 128 tokens).  The
+ * format is the library's own.  A token has an exponent e, each of its 32 groups
+ * of 16 latent channels an offset d, and
+ *   latent channel = E2M1 code * 2^(e + 6 - d)    (0, 1/2, 1, 3/2, 2, 3, 4, 6)
+ *   rope channel   = E4M3 code * 2^e
+ * The rope keeps 8 bits: positions are told apart by it.
+ *   cache      uint8 [n_blocks, block_size / 16, CPMLA_PAGED4_STRIP_BYTES]: strips
+ *              of 16 tokens.  With r = slot % 16 and strip slot / 16:
+ *     256 r + 16 (g % 16) + 8 (g / 16)   group g's 16 codes, two little-endian 32-
+ *              bit words of 8: channel j's magnitude code at bits 4j .. 4j + 2, its
+ *              sign at bit 8j + 7 (j < 4) or 8 (j - 4) + 3 (j >= 4)
+ *     4096 + 64 r    64 rope codes
+ *     5120 + 16 r    16 bytes: d[u] | d[u + 16] << 4; offsets above 11 are read as 11
+ *     5376 + r       e + 127, 63 .. 246; 255: every value is NaN; other bytes are
+ *              read as the nearest of 63 .. 246
+ *
+ * mla_paged4_cache_insert -- token t's row to slot slot_mapping[t].  e is the
+ * least exponent in -64 .. 119 with |x| <= 448 * 2^e for every finite channel, d
+ * the largest offset in 0 .. 11 with |x| <= 7 * 2^(e + 6 - d) for the group's
+ * finite ones; codes are the nearest, ties to the even code, and saturate
+ * (infinities become the largest).  A token with a NaN channel is NaN throughout.
+ * Tokens do not share scales: any order, and blocks may be written again in part.
+ *   kv, kv_token_stride, n, slot_mapping  as in 2g; slots must be distinct
+ *
+ * mla_paged4_cache_read -- the other way: kv[t, :] = the values of slot
+ * slot_mapping[t] (each exactly a bf16), zeros where it is -1.  Two entries may
+ * name one slot.  With the slots of a request's positions this is the contiguous
+ * latent KV that the prefill kernels take; with a step's own, what its rows attend
+ * to.
+ *   kv         bf16 [n, 576] output, rows kv_token_stride elements apart (host, >=
+ *              576, a multiple of 8); 16-byte aligned
+ * Both: a slot outside [-1, slots of the cache) is taken as -1 and recorded as
+ * CPMLA_ERR_INDEX in the status word; cache and kv 16-byte aligned.
+ *
+ * mla_paged4_attn -- mla_paged_attn over this cache: arguments, results, workspace
+ * (mla_paged_attn_workspace_size) and errors as there, without cache_exp.  What
+ * lies in the cache at positions that a row does not attend to does not reach it.
+ *
+ * All three: nothing is allocated, no host synchronisation, usable in stream
+ * capture.  Errors: CPMLA_ERR_ARG, CPMLA_ERR_UNSUPPORTED, CPMLA_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define CPMLA_PAGED4_STRIP_BYTES 5392
+
+int mla_paged4_cache_insert(const void *kv, int64_t kv_token_stride, int n,
+                            const int64_t *slot_mapping, void *cache, int n_blocks, int block_size,
+                            void *stream);
+
+int mla_paged4_cache_read(const void *cache, int n_blocks, int block_size,
+                          const int64_t *slot_mapping, int n, void *kv, int64_t kv_token_stride,
+                          void *stream);
+
+int mla_paged4_attn(const void *q, int64_t q_token_stride, int H, const void *cache, int n_blocks,
+                    int block_size, const int32_t *block_table, int B, int64_t table_stride,
+                    const int32_t *tokens, const int32_t *pos, const int32_t *req, int n_tokens,
+                    const int32_t *kv_lo, const int32_t *kv_hi, float softmax_scale,
+                    const float *sink, int T, void *o_out, float *lse_out, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
  * 3. Global LSE merge + attention sink once + restore to global order (device)
  *
  * "[DeepSeekV4][PCP] ...", "Implementation summary" (merge LSE/output
