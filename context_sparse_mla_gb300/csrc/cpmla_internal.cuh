@@ -174,6 +174,27 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *tm) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
 }
 
+// --- bulk copy global -> shared (no tensor map), completion on an mbarrier: both
+// addresses 16-byte aligned, bytes a multiple of 16
+__device__ __forceinline__ void bulk_load_g2s(void *dst, const void *src, uint32_t bytes,
+                                              uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// --- registers of a warpgroup, from and to those that the block was launched with
+template <int N>
+__device__ __forceinline__ void reg_alloc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dealloc() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // --- bulk copy shared -> global (TMA, no tensor map): both addresses 16-byte
 // aligned, bytes a multiple of 16
 __device__ __forceinline__ void bulk_store_s2g(void *gdst, const void *ssrc, uint32_t bytes) {
@@ -234,6 +255,19 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::mxf8f6f4: A and B from shared memory, each with a UE8M0 scale for a row and 32
+// of K, four to a 32-bit word of TMEM: row r's at lane r % 32 (the same in all quarters
+// of the lanes), column r / 32.
+__device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4],"
+      " [%5], p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
       : "memory");
 }
 // Arrive on an mbarrier once every tcgen05 operation issued so far by this
@@ -364,6 +398,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_
 __host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N, int a_mn, int b_mn) {
   return idesc_e4m3(M, N, a_mn, b_mn) | (1u << 10);
 }
+// kind::mxf8f6f4 with E4M3 A and B and UE8M0 scales, byte 0 of A's words; and which byte
+// of B's.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N, int a_mn, int b_mn) {
+  return ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+         (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_mx_b_scale(uint32_t byte) { return byte << 4; }
 // The same as idesc_bf16 with fp16 A and B (A/B format field 0).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |

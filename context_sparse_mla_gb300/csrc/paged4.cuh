@@ -33,6 +33,19 @@ __device__ __forceinline__ float p4_scale(int stored) {
   return __int_as_float(stored == kP4Nan ? 0x7FFFFFFF : s << 23);
 }
 
+// 16 channels of a group (two words of codes) as E4M3, for a token on the scale 2^e:
+// E2M1 * 2^(6 - d).  Magnitude 1/2 at offset d is the E4M3 code 8 (12 - d), and all
+// others lie above it by what they do at every d <= 11, so a group has one table.
+__device__ __forceinline__ uint4 p4_e4m3x16(uint32_t w0, uint32_t w1, uint32_t d) {
+  const uint32_t m = 8u * (12u - min(d, (uint32_t)kP4OffMax));
+  const uint32_t lo = 0x0C080000u + m * 0x01010100u, hi = 0x1C181410u + m * 0x01010101u;
+  const uint32_t s0 = w0 & 0x77777777u, s1 = w1 & 0x77777777u;
+  return make_uint4(__byte_perm(lo, hi, s0) | (w0 & 0x80808080u),
+                    __byte_perm(lo, hi, s0 >> 16) | (w0 << 4 & 0x80808080u),
+                    __byte_perm(lo, hi, s1) | (w1 & 0x80808080u),
+                    __byte_perm(lo, hi, s1 >> 16) | (w1 << 4 & 0x80808080u));
+}
+
 #endif  // __CUDACC__
 
 }  // namespace cpmla

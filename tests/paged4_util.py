@@ -112,7 +112,9 @@ def rotate(x, pos, f, amplitude=1.0, pairs=True, inverse=False):
 
 
 def attend(q, val, table, tokens, pos, req, scale, sink=None, lo=None, hi=None):
-    """As paged_util.attend, over values (float64 [n_blocks, bs, 576] on q's device)."""
+    """As paged_util.attend, over values (float64 [n_blocks, bs, 576] on q's device); the
+    weight's companion is the same sum with each weight replaced by the largest of its
+    tile of 64 positions."""
     dev = q.device
     n_blocks, bs = val.shape[:2]
     out = {}
@@ -133,7 +135,11 @@ def attend(q, val, table, tokens, pos, req, scale, sink=None, lo=None, hi=None):
         p = torch.exp(x - torch.where(lse.isinf(), 0.0, lse)[:, None])
         gate = torch.ones_like(lse) if sink is None else torch.sigmoid(lse - sink.double())
         p = p * torch.where(lse.isneginf(), 0.0, gate)[:, None]
-        out[i] = (p @ kv[:, :DV], lse, p @ kv[:, :DV].abs())
+        tile = k // 64 - (a // 64 if len(k) else 0)
+        big = torch.zeros((len(p), int(tile.max()) + 1 if len(k) else 1), dtype=p.dtype, device=dev)
+        big = big.index_reduce(1, tile, p, "amax")[:, tile]
+        v = kv[:, :DV].abs()
+        out[i] = (p @ kv[:, :DV], lse, p @ v, big @ v)
     return out
 
 
