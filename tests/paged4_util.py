@@ -111,12 +111,13 @@ def rotate(x, pos, f, amplitude=1.0, pairs=True, inverse=False):
     return np.concatenate([y.real, y.imag], -1)
 
 
-def attend(q, val, table, tokens, pos, req, scale, sink=None, lo=None, hi=None):
-    """As paged_util.attend, over values (float64 [n_blocks, bs, 576] on q's device); the
-    weight's companion is the same sum with each weight replaced by the largest of its
-    tile of 64 positions."""
+def attend(q, val, cache, table, tokens, pos, req, scale, sink=None, lo=None, hi=None):
+    """As paged_util.attend, over values (float64 [n_blocks, bs, 576] on q's device) of a
+    cache.  With P a weight times its token's 2^e, the weight's companion is the sum over
+    the tokens of the largest P of their 32 positions times their codes' magnitudes."""
     dev = q.device
     n_blocks, bs = val.shape[:2]
+    unit = cache[..., 5376:].reshape(n_blocks, bs).to(dev).double().clamp(63, 246).sub(127).exp2()
     out = {}
     for i in range(len(pos)):
         b, t = int(req[i]), int(pos[i])
@@ -135,11 +136,12 @@ def attend(q, val, table, tokens, pos, req, scale, sink=None, lo=None, hi=None):
         p = torch.exp(x - torch.where(lse.isinf(), 0.0, lse)[:, None])
         gate = torch.ones_like(lse) if sink is None else torch.sigmoid(lse - sink.double())
         p = p * torch.where(lse.isneginf(), 0.0, gate)[:, None]
-        tile = k // 64 - (a // 64 if len(k) else 0)
+        tile = k // 32 - (a // 32 if len(k) else 0)
         big = torch.zeros((len(p), int(tile.max()) + 1 if len(k) else 1), dtype=p.dtype, device=dev)
-        big = big.index_reduce(1, tile, p, "amax")[:, tile]
+        e = unit[blk, k % bs]
+        big = big.index_reduce(1, tile, p * e, "amax")[:, tile]
         v = kv[:, :DV].abs()
-        out[i] = (p @ kv[:, :DV], lse, p @ v, big @ v)
+        out[i] = (p @ kv[:, :DV], lse, p @ v, big @ (v / e[:, None]))
     return out
 
 

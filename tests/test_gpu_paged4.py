@@ -13,9 +13,10 @@ pytestmark = pytest.mark.gpu
 SCALE = 576 ** -0.5
 # Bounds of the attention, fixed from its arithmetic: binary32 sums of 576 products in
 # 20 steps; nine bits of a weight.  O_TILE is the least step's: a weight is two E4M3 on a
-# scale on which the largest of its row's 32 keys lies in (2^7, 2^8], and its second part
-# is off by up to half of E4M3's least step, 2^-10, so by 2^-17 of that largest.  (Many
-# E2M1 codes are 0: the heaviest keys of a tile may add nothing to a channel.)
+# scale on which the largest of its row's 32 keys (each times its token's 2^e, which the
+# weights carry) lies in (2^7, 2^8], and its second part is off by up to half of E4M3's
+# least step, 2^-10: by 2^-17 of that largest.  (Many E2M1 codes are 0: the heaviest keys
+# of a tile may add nothing to a channel.)
 LSE_ABS, LSE_REL = 1e-4, 2e-6
 O_REL, O_WEIGHT, O_TILE, O_NORM = 2.0 ** -8, 2.0 ** -7, 2.0 ** -17, 2.0 ** -8
 
@@ -306,7 +307,7 @@ def check_attn(d, val, q, o, lse, tokens=None, sink=None, lo=None, hi=None, stat
         keep = np.zeros(n, bool)
         keep[some] = True
         req[~keep] = -1
-    ref = p4.attend(q, val, d["block_table"], tok, pos, req, scale, sink, lo, hi)
+    ref = p4.attend(q, val, d["cache"], d["block_table"], tok, pos, req, scale, sink, lo, hi)
     assert cpmla.device_status() == status
     num = den = 0.0
     for i, (ro, rl, w, wt) in ref.items():
