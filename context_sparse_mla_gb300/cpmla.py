@@ -491,12 +491,16 @@ def rope_freqs(base=10000.0, *, factor=1.0, original_len=4096, beta_fast=32.0, b
 
 
 def _rope_view(t, n, dim, dev, name):
-    if (t.dtype is not torch.bfloat16 or t.dim() != dim or t.shape[0] != n
-            or t.shape[-1] != DROPE or t.stride(-1) != 1 or t.get_device() != dev):
+    shape, st = t.shape, t.stride()
+    if (t.dtype is not torch.bfloat16 or len(shape) != dim or shape[0] != n
+            or shape[-1] != DROPE or st[-1] != 1 or t.get_device() != dev):
         raise ValueError("%s must be a bfloat16 [%s64] view of contiguous channels on cuda:%d"
                          % (name, "%d, " % n if dim == 2 else "%d, H, " % n, dev))
     # strides of dimensions of one entry are never used, and may be anything
-    return (t.data_ptr(), *(s if d > 1 else DROPE for d, s in zip(t.shape[:-1], t.stride())))
+    token = st[0] if n > 1 else DROPE
+    if dim == 2:
+        return t.data_ptr(), token
+    return t.data_ptr(), token, st[1] if shape[1] > 1 else DROPE
 
 
 def mla_rope(q, pos, inv_freq, *, k=None, q_out=None, k_out=None, amplitude=1.0, interleaved=True,

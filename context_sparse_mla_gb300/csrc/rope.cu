@@ -17,6 +17,7 @@ namespace cpmla {
 namespace {
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopeRows = 20;  // of a warp: 16 heads and the key, 17, are one warp's
 constexpr int kRopePairs = CPMLA_DROPE / 2;
 
 struct RopeArgs {
@@ -24,7 +25,7 @@ struct RopeArgs {
   __nv_bfloat16 *qo, *ko;
   int64_t qt, qh, qot, qoh, kt, kot;
   int H, rows;  // heads of q; rows of a token (the heads, then the key)
-  int n, per;   // tokens; rows that a warp takes
+  int n, parts, per;  // tokens; a token's parts, of so many rows, a warp's work each
   const int32_t *pos;
   float amp;
   int halves, inverse;
@@ -35,20 +36,33 @@ struct RopeRow {
   uint2 a, b;  // first and second half, or channels 8 c .. + 3 and + 4 .. + 7
 };
 
+// A warp's work is per <= kRopeRows rows of a token, all loaded before the angle is known
+// (and the next position beside them): bound by HBM, with the rows' 128 bytes apart
+// (32,771 tokens of 16 heads and the key: 28 us, 5.1 TB/s; 43 with the angle first and the
+// 17th row behind the others).  Eight blocks an SM and a loop: 28 us, 31 without the loop.
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kU = kRopeRows / 4;
   const int lane = threadIdx.x & 31, c = lane & 7, g = lane >> 3;
-  const int n_part = (a.rows + a.per - 1) / a.per;
-  const int64_t n_work = (int64_t)a.n * n_part;
+  const int64_t n_work = (int64_t)a.n * a.parts;
   const int64_t n_warps = (int64_t)gridDim.x * (kRopeThreads / 32);
   const uint64_t turn = a.turns[4 * c + g];
   const int x0 = a.halves ? 4 * c : 8 * c, x1 = a.halves ? x0 + 32 : x0 + 4;
-  for (int64_t w = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); w < n_work;
-       w += n_warps) {
-    const int64_t t = w / n_part;
-    const int r0 = (int)(w - t * n_part) * a.per, r1 = min(r0 + a.per, a.rows);
-    const int p = a.pos[t];
-    if (p < 0) continue;
+  int64_t w = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  int p = w < n_work ? a.pos[w / a.parts] : -1;
+  while (w < n_work) {
+    const int64_t t = w / a.parts, nxt = w + n_warps;
+    const int r0 = (int)(w - t * a.parts) * a.per, r1 = min(r0 + a.per, a.rows);
+    RopeRow v[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + g + 4 * u;
+      if (r >= r1) break;
+      const __nv_bfloat16 *src = r < a.H ? a.q + t * a.qt + r * a.qh : a.k + t * a.kt;
+      v[u].a = *reinterpret_cast<const uint2 *>(src + x0);
+      v[u].b = *reinterpret_cast<const uint2 *>(src + x1);
+    }
+    const int p_nxt = nxt < n_work ? a.pos[nxt / a.parts] : -1;
     float s, co;
     sincospif((float)(int64_t)((uint64_t)p * turn) * 0x1p-63f, &s, &co);
     co *= a.amp;
@@ -59,54 +73,44 @@ __global__ void __launch_bounds__(kRopeThreads)
       cs[i] = __shfl_sync(0xffffffffu, co, 8 * i + c);
       sn[i] = __shfl_sync(0xffffffffu, s, 8 * i + c);
     }
-    constexpr int kU = 4;
-    for (int r = r0 + g; r < r1; r += 4 * kU) {
-      RopeRow v[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int rr = r + 4 * u;
-        if (rr >= r1) break;
-        const __nv_bfloat16 *src = rr < a.H ? a.q + t * a.qt + rr * a.qh : a.k + t * a.kt;
-        v[u].a = *reinterpret_cast<const uint2 *>(src + x0);
-        v[u].b = *reinterpret_cast<const uint2 *>(src + x1);
-      }
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + g + 4 * u;
+      if (r >= r1 || p < 0) break;
+      // the four pairs' first and second channels
+      float x[4], y[4];
+      const uint32_t wd[4] = {v[u].a.x, v[u].a.y, v[u].b.x, v[u].b.y};
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int rr = r + 4 * u;
-        if (rr >= r1) break;
-        // the four pairs' first and second channels
-        float x[4], y[4];
-        const uint32_t wd[4] = {v[u].a.x, v[u].a.y, v[u].b.x, v[u].b.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = __uint_as_float(wd[i] << 16), hi = __uint_as_float(wd[i] & 0xFFFF0000u);
-          if (a.halves) {
-            (i < 2 ? x : y)[2 * i & 3] = lo;
-            (i < 2 ? x : y)[(2 * i & 3) + 1] = hi;
-          } else {
-            x[i] = lo;
-            y[i] = hi;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float nx = fmaf(x[i], cs[i], -(y[i] * sn[i]));
-          y[i] = fmaf(x[i], sn[i], y[i] * cs[i]);
-          x[i] = nx;
-        }
-        RopeRow o;
+      for (int i = 0; i < 4; ++i) {
+        const float lo = __uint_as_float(wd[i] << 16), hi = __uint_as_float(wd[i] & 0xFFFF0000u);
         if (a.halves) {
-          o.a = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-          o.b = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+          (i < 2 ? x : y)[2 * i & 3] = lo;
+          (i < 2 ? x : y)[(2 * i & 3) + 1] = hi;
         } else {
-          o.a = make_uint2(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1]));
-          o.b = make_uint2(pack_bf16x2(x[2], y[2]), pack_bf16x2(x[3], y[3]));
+          x[i] = lo;
+          y[i] = hi;
         }
-        __nv_bfloat16 *dst = rr < a.H ? a.qo + t * a.qot + rr * a.qoh : a.ko + t * a.kot;
-        *reinterpret_cast<uint2 *>(dst + x0) = o.a;
-        *reinterpret_cast<uint2 *>(dst + x1) = o.b;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float nx = fmaf(x[i], cs[i], -(y[i] * sn[i]));
+        y[i] = fmaf(x[i], sn[i], y[i] * cs[i]);
+        x[i] = nx;
+      }
+      RopeRow o;
+      if (a.halves) {
+        o.a = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        o.b = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      } else {
+        o.a = make_uint2(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1]));
+        o.b = make_uint2(pack_bf16x2(x[2], y[2]), pack_bf16x2(x[3], y[3]));
+      }
+      __nv_bfloat16 *dst = r < a.H ? a.qo + t * a.qot + r * a.qoh : a.ko + t * a.kot;
+      *reinterpret_cast<uint2 *>(dst + x0) = o.a;
+      *reinterpret_cast<uint2 *>(dst + x1) = o.b;
     }
+    w = nxt;
+    p = p_nxt;
   }
 }
 
@@ -205,10 +209,11 @@ extern "C" int mla_rope(const void *q, int64_t q_token_stride, int64_t q_head_st
   a.halves = layout == CPMLA_ROPE_HALVES;
   a.inverse = inverse != 0;
   for (int i = 0; i < kRopePairs; ++i) a.turns[i] = turns_of(inv_freq[i]);
-  a.per = 32;
-  const int64_t warps = (int64_t)n * ((a.rows + a.per - 1) / a.per);
+  a.parts = (a.rows + kRopeRows - 1) / kRopeRows;
+  a.per = (a.rows + a.parts - 1) / a.parts;
+  const int64_t warps = (int64_t)n * a.parts;
   const int64_t grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  rope_kernel<<<(unsigned)(grid < 152 * 16 ? grid : 152 * 16), kRopeThreads, 0,
+  rope_kernel<<<(unsigned)(grid < 152 * 8 ? grid : 152 * 8), kRopeThreads, 0,
                 static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "mla_rope: launch");
