@@ -271,53 +271,34 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
       : "memory");
 }
 
-// The same, called by a whole converged warp: one lane, the same at every call, issues.
-// (Operands stay in uniform registers: 32 cycles a MMA, where one lane behind a branch
-// takes 65.)
-#define CPMLA_ELECT(setp) "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n" setp
-__device__ __forceinline__ void mma_f8_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
-  asm volatile(CPMLA_ELECT(" setp.ne.b32 p, %4, 0;\n")
-               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-               : "memory");
-}
-__device__ __forceinline__ void mma_f8_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
-  asm volatile(CPMLA_ELECT(" setp.ne.b32 p, %4, 0;\n")
-               " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-                   d_tmem),
-               "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-               : "memory");
-}
 // kind::mxf8f6f4: A and B from shared memory, each with a UE8M0 scale for a row and 32
 // of K, four to a 32-bit word of TMEM: row r's at lane r % 32 (the same in all quarters
 // of the lanes), column r / 32.
-__device__ __forceinline__ void mma_mx_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
-                                               uint32_t accumulate) {
+__device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                          uint32_t accumulate) {
   asm volatile(
-      CPMLA_ELECT(" setp.ne.b32 p, %6, 0;\n")
-      " @q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4],"
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4],"
       " [%5], p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
       : "memory");
 }
 // 32 rows of 16 bytes, side by side in shared memory, to four columns of each quarter of
-// the lanes; in order with the issuing lane's MMAs.
-__device__ __forceinline__ void tmem_cp_32x128b_warp(uint32_t d_tmem, uint64_t s_desc) {
-  asm volatile(CPMLA_ELECT("") " @q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(
-                   d_tmem),
-               "l"(s_desc)
+// the lanes; in order with the issuing thread's MMAs.
+__device__ __forceinline__ void tmem_cp_32x128b(uint32_t d_tmem, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(s_desc)
                : "memory");
 }
-__device__ __forceinline__ void mma_commit_warp(uint64_t *bar) {
-  asm volatile(CPMLA_ELECT("")
-               " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
-               "[%0];\n}\n" ::"r"(smem_u32(bar))
-               : "memory");
+// True for one lane of a converged warp, the same at every call.  A tile's MMAs behind one
+// `if (elect_one())` are issued in half of the instructions that an election for each, or
+// `if (lane == 0)`, takes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r));
+  return r != 0;
 }
-#undef CPMLA_ELECT
 
 // --- TMEM <-> registers, 32 lanes x 32 bit, 16 columns per call
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {

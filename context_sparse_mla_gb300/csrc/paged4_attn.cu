@@ -44,7 +44,7 @@ constexpr int kP4Pack = kPgTile / 16 * kStrip;    // a tile's strips
 constexpr int kP4Fetch = 6;
 // Registers a thread by warpgroup, dealt out anew from the 80 that 768 threads are
 // launched with: a tile's scores of a thread are 32, a strip's share 48.
-constexpr int kP4Regs = 80, kP4RegsCtl = 48, kP4RegsSoftmax = 104, kP4RegsQ = 64, kP4RegsX = 80;
+constexpr int kP4Regs = 80, kP4RegsCtl = 48, kP4RegsSoftmax = 112, kP4RegsQ = 64, kP4RegsX = 72;
 static_assert(kP4RegsCtl + 2 * kP4RegsSoftmax + kP4RegsQ + 2 * kP4RegsX <= 6 * kP4Regs,
               "shares of what the block is launched with");
 
@@ -192,7 +192,10 @@ __global__ void __launch_bounds__(kP4Threads, 1)
   uint8_t *sPack = sRope + NR * kPgRope;  // strips as they lie in the cache
   P4Ctrl<R> &c = *reinterpret_cast<P4Ctrl<R> *>(
       ((uintptr_t)sPack + NP * kP4Pack + 127) & ~(uintptr_t)127);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (what a shuffle from one lane gives is known to be the same in all: roles' branches and
+  // MMAs' operands in uniform registers)
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
   __syncthreads();
   tc_fence_after();
   grid_dependency_wait();  // the plan is there
-  const uint32_t tmem = c.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem_base, 0);
   // S buffer b at tS + 64 b, O^T chunk ch at tO + kOW ch
   const uint32_t tS = tmem + Cfg::kColS, tO = tmem + Cfg::kColO;
   const uint32_t tSA = tmem + Cfg::kColScale, tSB = tSA + 4;
@@ -257,24 +260,27 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           tc_fence_after();
           const uint64_t db = dr + ((slot * kP4Tile) >> 4);
           const uint64_t drb = drr + ((j % NR * kPgRope) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int n = 0; n < 18; ++n) {
-            const uint64_t b = n < 16 ? db + ((n / 4 * kPgSlot + n % 4 * 32) >> 4)
-                                      : drb + (((n - 16) * 32) >> 4);
-            const int i = n - Cfg::kQSteps;  // behind q's in TMEM: pairs in shared memory
-            if (i < 0)
-              mma_f8_ts_warp(dS, tmem + n * 8, b, id, n != 0 ? 1u : 0u);
-            else
-              mma_f8_ss_warp(dS, dqr + ((i / 2 * Cfg::kQPair + i % 2 * 32) >> 4), b, id, 1u);
+            for (int n = 0; n < 18; ++n) {
+              const uint64_t b = n < 16 ? db + ((n / 4 * kPgSlot + n % 4 * 32) >> 4)
+                                        : drb + (((n - 16) * 32) >> 4);
+              const int i = n - Cfg::kQSteps;  // behind q's in TMEM: pairs in shared memory
+              if (i < 0)
+                mma_f8_ts(dS, tmem + n * 8, b, id, n != 0 ? 1u : 0u);
+              else
+                mma_f8_ss(dS, dqr + ((i / 2 * Cfg::kQPair + i % 2 * 32) >> 4), b, id, 1u);
+            }
+            mma_commit(&c.s_full[j & 1]);
+            mma_commit(&c.rope_free[j % NR]);
           }
-          mma_commit_warp(&c.s_full[j & 1]);
-          mma_commit_warp(&c.rope_free[j % NR]);
+          __syncwarp();
         }
-        if (ok) mma_commit_warp(&c.q_free);
+        if (ok && elect_one()) mma_commit(&c.q_free);
         ++piece;
       }
       if (!ok) {
-        mma_commit_warp(&c.drain[warp]);
+        if (elect_one()) mma_commit(&c.drain[warp]);
         pg_drain(&c.drain[warp], 0, kWaitLimitNs);
       }
       __syncwarp();
@@ -298,32 +304,35 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           ok = warp_wait(&c.p_full[b], (j >> 1) & 1, abort, a.status);
           if (!ok) break;
           tc_fence_after();
-          // (the scales of the tile before are read: a thread's copies and MMAs are in order)
-          tmem_cp_32x128b_warp(tSB + 4 * me, df + ((b * sizeof c.sf[0]) >> 4));
+          if (elect_one()) {
+            // (the scales of the tile before are read: a thread's copies and MMAs are in order)
+            tmem_cp_32x128b(tSB + 4 * me, df + ((b * sizeof c.sf[0]) >> 4));
 #pragma unroll
-          for (int cx = 0; cx < 4 / Cfg::kPvW; ++cx) {
-            const int ch = me + Cfg::kPvW * cx;
-            const uint64_t da = dr + ((j % NS * kP4Tile + ch * kPgSlot) >> 4);
-            uint32_t acc = t > w.t0 ? 1u : 0u;
+            for (int cx = 0; cx < 4 / Cfg::kPvW; ++cx) {
+              const int ch = me + Cfg::kPvW * cx;
+              const uint64_t da = dr + ((j % NS * kP4Tile + ch * kPgSlot) >> 4);
+              uint32_t acc = t > w.t0 ? 1u : 0u;
 #pragma unroll
-            for (uint32_t k = 0; k < kPgTile / 32; ++k)
+              for (uint32_t k = 0; k < kPgTile / 32; ++k)
 #pragma unroll
-              for (uint32_t y = 0; y < 2; y += W) {
-                const uint64_t db = dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4);
-                // (a byte of a row's scales for each 32 keys)
-                mma_mx_ss_warp(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4), db,
-                               id | idesc_mx_b_scale(k), tSA, tSB + 4 * me, acc);
-                acc = 1;
-              }
+                for (uint32_t y = 0; y < 2; y += W) {
+                  const uint64_t db = dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4);
+                  // (a byte of a row's scales for each 32 keys)
+                  mma_mx_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4), db,
+                            id | idesc_mx_b_scale(k), tSA, tSB + 4 * me, acc);
+                  acc = 1;
+                }
+            }
+            mma_commit(&c.empty[j % NS]);
+            mma_commit(&c.p_free[b]);
           }
-          mma_commit_warp(&c.empty[j % NS]);
-          mma_commit_warp(&c.p_free[b]);
+          __syncwarp();
         }
-        if (ok) mma_commit_warp(&c.o_full);
+        if (ok && elect_one()) mma_commit(&c.o_full);
         ++piece;
       }
       if (!ok) {
-        mma_commit_warp(&c.drain[warp]);
+        if (elect_one()) mma_commit(&c.drain[warp]);
         pg_drain(&c.drain[warp], 0, kWaitLimitNs);
       }
       __syncwarp();
@@ -404,6 +413,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
     const float one = __uint_as_float(0x7F7F7F7Fu), ones[4] = {one, one, one, one};
     if (wg == 0) tmem_st4(tSA + lane_off, ones);
     tmem_st_wait();
+    tc_fence_before();
     // a piece's bounds for this thread's row; asked for before the output of the piece ahead
     bool mine = false;
     int lo = 1, hi = 0, x = 0;
@@ -917,16 +927,11 @@ __global__ void __launch_bounds__(kP4Threads, 1)
                        ((half ? j / NR : j / NS) & 1) ^ 1, abort, a.status);
         if (!ok) break;
         uint8_t *dst = sRing + es * kP4Tile + (u >> 3) * kPgSlot + (k0 + half) * 128;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h, dst += 1024) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint8_t *d = dst + i * 256 + (((u & 7) ^ (2 * i + half)) << 4);
-            *reinterpret_cast<uint4 *>(d) = p4_e4m3x16(v[i].x, v[i].y, off[i] & 15);
-            *reinterpret_cast<uint4 *>(d + 2 * kPgSlot) = p4_e4m3x16(v[i].z, v[i].w, off[i] >> 4);
-            v[i] = v[i + 4];
-            off[i] = off[i + 4];
-          }
+        for (int i = 0; i < 8; ++i) {
+          uint8_t *d = dst + i * 256 + (((u & 7) ^ (2 * (i & 3) + half)) << 4);
+          *reinterpret_cast<uint4 *>(d) = p4_e4m3x16(v[i].x, v[i].y, off[i] & 15);
+          *reinterpret_cast<uint4 *>(d + 2 * kPgSlot) = p4_e4m3x16(v[i].z, v[i].w, off[i] >> 4);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
