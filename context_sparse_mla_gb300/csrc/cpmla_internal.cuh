@@ -185,11 +185,6 @@ __device__ __forceinline__ void bulk_load_g2s(void *dst, const void *src, uint32
       : "memory");
 }
 
-// ... and into L2 only.
-__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 // --- registers of a warpgroup, from and to those that the block was launched with
 template <int N>
 __device__ __forceinline__ void reg_alloc() {

@@ -19,15 +19,20 @@
 // the output, 12-15 bring q in, 16-23 expand.  Every wait is bounded; on expiry the CTA
 // records CPMLA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 //
-// What bounds it, measured.  Instructions: a tile is 5,000 (R = 16) or 7,000 of them, half
-// of them of the pipe that takes one every two cycles; the expansion alone is 365 for each
-// scheduler, 730 cycles.  A tile takes 2,000 and 2,600 cycles (32 tokens of 4,096 to
-// 131,072 keys: 211 us with 16 heads, 3.2 TB/s; 290 with 64; the 8-bit cache's 216 and
-// 266), of which shared memory is busy for 1,300 and 1,900 and the tensor core for 800 and
-// 1,300.  What was worth most on the way: roles' loops that fit the instruction cache
-// together; a wait of all lanes (an issue of what follows, not two); MMAs issued from
-// uniform registers; a reference that never moves in practice; tiles expanded by two groups
-// in turn.
+// What bounds it, measured (32 tokens of 4,096 to 131,072 keys).  R = 16: 184 us a call
+// with 16 heads, 3.6 TB/s (the 8-bit cache's 212, 5.2 TB/s); R = 64: 266 us with 64 heads,
+// 1.04 PFLOP/s of the exact products (270).  A tile takes 1,700 and 2,450 cycles.  Shared
+// memory is busy for 1,300 and 1,900 of them, the tensor core for 800 and 1,300, and a
+// scheduler issues 1,250 and 1,550 instructions, half of them of the pipe that takes one
+// every two cycles (the expansion alone 730 cycles).  None of these fills the time: a tile
+// keeps its place in the ring for the chain of its expansion, scores, softmax and PV, 8,300
+// and 9,700 cycles, and there are places for 5 and 4.  8,192 prompt tokens of 16 heads
+// 1,200 us (1,160).  On the way here: the roles' loops have to fit the instruction cache
+// together (a softmax loop with 32 keys side by side instead of 16: 680 us for the 64
+// heads); a wait by one lane leaves its warp apart, and what follows is issued twice (484,
+// 398); a tile's MMAs behind one election (266, 325 with one for each); a reference that
+// next to never moves (257, 394 with moves beyond 28); strips taken into registers at once,
+// by two groups of warps in turn.
 #include <type_traits>
 
 #include "paged4.cuh"
@@ -39,9 +44,6 @@ namespace {
 constexpr int kP4Threads = 768;   // warpgroups: control, two softmax, q, two that expand
 constexpr int kP4Tile = 4 * kPgSlot;              // ring slot: a tile's latent chunks
 constexpr int kP4Pack = kPgTile / 16 * kStrip;    // a tile's strips
-// Tiles that strips are asked for into L2 ahead of their copies, so that two places for
-// them suffice (32 rows of 16 heads: 211 us; 253 without, the copies 2,600 cycles each).
-constexpr int kP4Fetch = 6;
 // Registers a thread by warpgroup, dealt out anew from the 80 that 768 threads are
 // launched with: a tile's scores of a thread are 32, a strip's share 48.
 constexpr int kP4Regs = 80, kP4RegsCtl = 48, kP4RegsSoftmax = 112, kP4RegsQ = 64, kP4RegsX = 72;
@@ -60,8 +62,8 @@ struct P4Cfg {
   static constexpr int kPvW = R == 64 ? 2 : 1, kQkW = 3 - kPvW;
   // R = 16: q lies in each quarter of the lanes, so that any warp has the scores of all
   // rows: two of a softmax warpgroup take 32 of the tile's keys each, others than the
-  // other warpgroup's, so that every scheduler has one (211 us; 228 with the same two,
-  // and 276 with one warp a tile).
+  // other warpgroup's, so that every scheduler has one (189 us for the 32 tokens of 16
+  // heads; 191 with the same two, and with one warp a tile 276 where this was 228).
   static constexpr bool kSplit = R == 16;
   static constexpr int kLanes = kSplit ? 2 * R : R;  // rows and their copies
   static constexpr int kLive = kLanes / 16;          // warps of a warpgroup that have rows
@@ -84,10 +86,13 @@ struct P4Cfg {
 };
 // 2^e, e and 2^-e of a tile's keys (the upper half moved by 16 bytes: two threads' loads
 // of 32 keys apart share no bank), and its groups of 16 keys that have a page.
+constexpr int kP4High = 26;
 __host__ __device__ constexpr int p4_key(int k) { return k + (k >> 5) * 4; }
 struct P4KeyScale {
   float up[p4_key(kPgTile)], e[p4_key(kPgTile)], down[p4_key(kPgTile)];
-  uint32_t there, pad[3];
+  alignas(8) uint32_t there;
+  uint8_t high[4];  // a strip has a token of e > kP4High
+  uint32_t pad[2];
 };
 
 template <int R>
@@ -175,9 +180,52 @@ __device__ __forceinline__ uint2 split_p4(uint32_t x, uint32_t y) {
 // moves when a tile's largest lies kP4Up above it; a sum of 2^30 values stays below
 // 2^(30 + 9 + 80), and of a tile that lies so far below that its weights lose bits (72
 // under the first) nothing reaches binary32.  m never goes down.  (With m 6 below the first
-// tile's largest and moves 28 above it, for one sum on m, each row moved now and then:
-// of 64 rows' tiles every eighth waited for the PV GEMM, at 6,800 cycles each.)
+// tile's largest and moves 28 above it each row moves now and then, and every eighth tile
+// of 64 rows waits for the PV GEMM: 394 us where this takes 257.)
 constexpr float kP4Over = 40.f, kP4Up = 80.f;
+// What a thread's n keys need in the tiles that few are: those of an open end, with a page
+// that is not there, or with a value of 2^26 and more.  Out of line, as the roles' loops
+// fill the instruction cache.
+// u: position p .. of the keys; those outside lo .. hi, or in a group of 16 without a bit of
+// there, become -inf (a group that the row attends to and that is not there is a bad one:
+// between the ranges of two rows of a piece a block may be anything).  Returns the largest
+// u.  Behind the n: the largest t = u - e, the sum of 2^(t - max), and 1 if a key that is
+// left has e > kP4High.
+__device__ __noinline__ float p4_rare(float *u, const float *e, int n, int p, int lo, int hi,
+                                      uint32_t there, int *status) {
+  float top = -INFINITY, t_max = -INFINITY, t_sum = 0.f;
+  bool wide = false;
+#pragma unroll 1
+  for (int g = 0; g < n; g += 16) {
+    const bool gone = ((there >> (g >> 4)) & 1) == 0;
+    if (gone && max(lo, p + g) <= min(hi, p + g + 15)) record_status(status, CPMLA_ERR_INDEX);
+    const int from = gone ? 16 : lo - p - g, to = hi - p - g;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const float v = i < from || i > to ? -INFINITY : u[g + i];
+      u[g + i] = v;
+      top = fmaxf(top, v);
+      t_max = fmaxf(t_max, v - e[g + i]);
+      wide |= v > -INFINITY && e[g + i] > (float)kP4High;
+    }
+  }
+  u[n + 2] = wide ? 1.f : 0.f;
+  if (t_max == -INFINITY) t_max = 0.f;
+  u[n] = t_max;
+  if (__any_sync(0xffffffffu, wide))
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) t_sum += fast_exp2(u[i] - e[i] - t_max);
+  u[n + 1] = t_sum;
+  return top;
+}
+// The sum of 2^t and its reference behind a tile with wide exponents: of what they were
+// ahead of it (l.x on l.y) and p4_rare's sum; else what they have become (d).
+__device__ __noinline__ float2 p4_wide(const float *rare, float2 l, float2 d) {
+  if (rare[2] == 0.f) return d;
+  const float m = fmaxf(l.y, rare[0]);
+  return make_float2(pg_scale(l.x, l.y - m) + pg_scale(rare[1], rare[0] - m), m);
+}
+
 template <int R>
 __global__ void __launch_bounds__(kP4Threads, 1)
     paged4_attn_kernel(const __grid_constant__ PagedArgs a) {
@@ -346,9 +394,6 @@ __global__ void __launch_bounds__(kP4Threads, 1)
       uint32_t j = 0;
       while (ok && w.next(a)) {
         const int32_t *row = a.table + (int64_t)w.m.req * a.stride;
-        auto prefetch = [&](int y) {
-          if (y >= 0) bulk_prefetch(a.strips + (int64_t)(y >> 4) * kStrip, page_bytes);
-        };
         // first row in the cache of this lane's page, or -1
         auto page = [&](int t) {
           const int p0 = ((w.m.t_lo + t) << kPgTileLog) + lane * rows;
@@ -356,13 +401,10 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           const int blk = row[p0 >> a.shift];
           return blk >= 0 && blk < a.n_blocks ? (blk << a.shift) + (p0 & (bs - 1)) : -1;
         };
-        int far = w.t0;
-        for (; far < min(w.t0 + kP4Fetch, w.t1); ++far) prefetch(page(far));
         int nxt = page(w.t0);
         for (int t = w.t0; t < w.t1; ++t, ++j) {
           const int y = nxt;
           nxt = page(t + 1);
-          if (far < w.t1) prefetch(page(far++));
           const uint32_t slot = j % NP;
           // (groups of 16 keys that are there: a page is 1, 2 or 4 of them)
           uint32_t there = __ballot_sync(0xffffffffu, y >= 0);
@@ -446,6 +488,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
         constexpr int kHalf = kSplit ? 16 : 32;  // columns from lane to lane + 16
         const P4KeyScale &ks = c.ks[jj % NS];
         float u[kU], bt = -INFINITY;
+        float rare[kU + 3];  // (in local memory: out-of-line code alone uses it)
         auto turn = [&](const float *last) {  // the steps of u by one, with a new last one
 #pragma unroll
           for (int n = 0; n + kK < kU; ++n) u[n] = u[n + kK];
@@ -479,26 +522,15 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           tc_fence_before();
           warp_arrive(&c.s_free[wg], lane);
           const int p0 = (w.m.t_lo + x) << kPgTileLog;
-          const uint32_t there = ks.there;
-          if (there != 15u || p0 < w.m.lo_max || p0 + kPgTile - 1 > w.m.hi_min) {
-            bt = -INFINITY;
-#pragma unroll 1
-            for (int g = 0; g < kSteps; ++g) {
-              // a page without a block that the row attends to: its block is a bad one
-              // (between the ranges of two rows of a piece a block may be anything)
-              const int p = p0 + kb + kK * g;
-              const bool gone = ((there >> ((kb + kK * g) >> 4)) & 1) == 0;
-              if (gone && max(lo, p) <= min(hi, p + kK - 1))
-                record_status(a.status, CPMLA_ERR_INDEX);
-              const int from = gone ? kK : lo - p, to = hi - p;
-              float s[kK];
+          const uint2 th = *reinterpret_cast<const uint2 *>(&ks.there);
+          const uint32_t there = th.x;
+          if (((there ^ 15u) | th.y) != 0 || p0 < w.m.lo_max || p0 + kPgTile - 1 > w.m.hi_min) {
 #pragma unroll
-              for (int n = 0; n < kK; ++n) {
-                s[n] = n < from || n > to ? -INFINITY : u[n];
-                bt = fmaxf(bt, s[n]);
-              }
-              turn(s);
-            }
+            for (int n = 0; n < kU; ++n) rare[n] = u[n];
+            bt = p4_rare(rare, ks.e + p4_key(kb), kU, p0 + kb, lo, hi, there >> (kb >> 4), a.status);
+#pragma unroll
+            for (int n = 0; n < kU; ++n) u[n] = rare[n];
+            if (kSplit) rare[kU + 2] += __shfl_xor_sync(0xffffffffu, rare[kU + 2], 16);
           }
         }
         // the largest u of the 32 keys that share a scale, and what the warp has of the row
@@ -522,7 +554,9 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           if (mine && um > -INFINITY && um - m_old > kP4Up) m_new = ceilf(um) + kP4Over;
           const bool moved = live && m_old > -INFINITY && m_new != m_old;
           const uint32_t mv = __ballot_sync(0xffffffffu, moved);
-          if (live && lane < 16) c.alpha[wg][r] = moved ? fast_exp2(m_old - m_new) : 1.f;
+          // (half of the exponent, twice: m may rise by more than binary32's 126 where what O^T
+          // holds is 2^-7 of what comes)
+          if (live && lane < 16) c.alpha[wg][r] = moved ? fast_exp2(0.5f * (m_old - m_new)) : 1.f;
           if (lane == 0) c.mv[wg][q4] = mv;
           named_bar_sync(bar_wg, 128);
           if ((c.mv[wg][0] | c.mv[wg][1] | c.mv[wg][2] | c.mv[wg][3]) != 0) {
@@ -541,8 +575,10 @@ __global__ void __launch_bounds__(kP4Threads, 1)
                   tmem_ld16(tO + lane_off + cc * R + qr * 16, o);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    o[i] = o[i] == 0.f ? 0.f : o[i] * c.alpha[wg][qr * 16 + i];
+                  for (int i = 0; i < 16; ++i) {
+                    const float h = c.alpha[wg][qr * 16 + i];
+                    o[i] = o[i] == 0.f ? 0.f : o[i] * h * h;
+                  }
                   tmem_st16(tO + lane_off + cc * R + qr * 16, o);
                 }
               }
@@ -557,7 +593,9 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           if (ok) warp_arrive(&c.ref[qi], lane);
           // p = 2^(u - m) of 32 keys is p' = 2^(u - sub), at most 2^8, times 2^(sub - m)
           const bool some_key = mine && bt > -INFINITY;
-          const float sub = some_key ? fmaxf(ceilf(bt) - 8.f, m_new - 120.f) : 0.f;
+          // (from 2^27 on the difference is rounded, to 16 too, which an E4M3 does not hold)
+          const float top = bt - (ceilf(bt) - 8.f) > 8.f ? bt : ceilf(bt) - 8.f;
+          const float sub = some_key ? fmaxf(top, m_new - 120.f) : 0.f;
           // the PV GEMM of this buffer's last tile is done with it
           if (ok && jj >= 2)
             ok = warp_wait(&c.p_free[wg], ((jj >> 1) - 1) & 1, abort, a.status);
@@ -600,17 +638,26 @@ __global__ void __launch_bounds__(kP4Threads, 1)
 #pragma unroll
               for (int n = 0; n + kK < kU; ++n) u[n] = u[n + kK];
             }
+            const bool high = *reinterpret_cast<const uint32_t *>(ks.high) != 0;
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&c.p_full[wg], lane);
             // the sum of 2^t goes by a reference of its own (values and weights may lie
             // 183 binades apart)
+            const float2 was = make_float2(l, m_own);
             const float lr = some_key ? fmaxf(m_own, sub) : m_own;
             if (lr != m_own) {
               l = pg_scale(l, m_own - lr);
               m_own = lr;
             }
             l += pg_scale(sum[0] + sum[1], sub - lr);
+            // (2^t of the keys is p' 2^(sub - e), and p' keeps all of it where the exponents of
+            // the 32 lie at most 90 apart: none is above kP4High)
+            if (high) {
+              const float2 x = p4_wide(rare + kU, was, make_float2(l, m_own));
+              l = x.x;
+              m_own = x.y;
+            }
           }
         }
       }
@@ -667,7 +714,9 @@ __global__ void __launch_bounds__(kP4Threads, 1)
               orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
               if (q4 == 0) a.lse[orow] = L;
             } else if (q4 == 0) {
-              a.lse_part[(int64_t)part * R + rr] = l2;
+              // (a sum that is NaN on no reference)
+              a.lse_part[(int64_t)part * R + rr] =
+                  make_float2(sl != sl ? 0.f : ml, empty ? 0.f : log2f(sl));
             }
           }
           c.inv[sw][lane] = f;
@@ -927,11 +976,17 @@ __global__ void __launch_bounds__(kP4Threads, 1)
                        ((half ? j / NR : j / NS) & 1) ^ 1, abort, a.status);
         if (!ok) break;
         uint8_t *dst = sRing + es * kP4Tile + (u >> 3) * kPgSlot + (k0 + half) * 128;
+        // (four tokens a turn: 8,192 prompt tokens 1,197 us, 1,220 with all eight side by side)
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h, dst += 1024) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint8_t *d = dst + i * 256 + (((u & 7) ^ (2 * (i & 3) + half)) << 4);
-          *reinterpret_cast<uint4 *>(d) = p4_e4m3x16(v[i].x, v[i].y, off[i] & 15);
-          *reinterpret_cast<uint4 *>(d + 2 * kPgSlot) = p4_e4m3x16(v[i].z, v[i].w, off[i] >> 4);
+          for (int i = 0; i < 4; ++i) {
+            uint8_t *d = dst + i * 256 + (((u & 7) ^ (2 * i + half)) << 4);
+            *reinterpret_cast<uint4 *>(d) = p4_e4m3x16(v[i].x, v[i].y, off[i] & 15);
+            *reinterpret_cast<uint4 *>(d + 2 * kPgSlot) = p4_e4m3x16(v[i].z, v[i].w, off[i] >> 4);
+            v[i] = v[i + 4];
+            off[i] = off[i + 4];
+          }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -949,6 +1004,8 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           ks.down[k] = __uint_as_float((254u << 23) - __float_as_uint(up));
           ks.there = there;
         }
+        const bool high = __any_sync(0xffffffffu, e - 127 > kP4High);
+        if (lane == 0) ks.high[xw] = high;
         fence_proxy_async_smem();
         warp_arrive(&c.full[es], lane);
       }

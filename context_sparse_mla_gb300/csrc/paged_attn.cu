@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               orow = (int64_t)(a.tokens ? a.tokens[i] : i) * a.H + hh;
               if (q4 == 0) a.lse[orow] = L;
             } else if (q4 == 0) {
-              a.lse_part[(int64_t)part * R + rr] = l2;
+              a.lse_part[(int64_t)part * R + rr] = make_float2(l2, 0.f);
             }
           }
           c.inv[sw][lane] = f;

@@ -50,7 +50,9 @@ struct PagedArgs {
                     // cut: (group, head group, first CTA, parts), (first entry, rows, -, -);
                     // short ones from the front, those of many parts from the back
   float *o_part;    // [2 kPgMaxCtas][R][512]
-  float *lse_part;  // [2 kPgMaxCtas][R], base 2
+  // [2 kPgMaxCtas][R]: a part's LSE, base 2, as a reference (-inf: no key) and what lies
+  // above it (4 bits: log2 of the sum, which a reference of 2^24 and more would swallow)
+  float2 *lse_part;
   int *status;
 };
 
@@ -322,7 +324,7 @@ template <int R>
 struct PgJoin {
   static constexpr int kL = (kPgMaxCtas + 31) / 32, kAhead = 2;
   float4 o[4];
-  float mx, l;
+  float mx, above, l;  // the row's LSE is mx + above + log2 l
   int h;
   int64_t orow;  // the row of the output
   __device__ __forceinline__ PgJoin(const PagedArgs &a, const int4 &jn, const int4 &jg, int r,
@@ -341,19 +343,29 @@ struct PgJoin {
     const int e = jg.x + r / a.hc;
     h = jn.y * a.hc + r % a.hc;
     orow = (int64_t)(a.tokens ? a.tokens[e] : e) * a.H + h;
+    float2 s[kL];
     float p[kL];
-    mx = -INFINITY;
+    mx = above = -INFINITY;
     l = 0.f;
 #pragma unroll
     for (int k = 0; k < kL; ++k) {
-      p[k] = lane + 32 * k < n ? __ldcg(a.lse_part + at(lane + 32 * k)) : -INFINITY;
-      mx = fmaxf(mx, p[k]);
+      s[k] = lane + 32 * k < n ? __ldcg(a.lse_part + at(lane + 32 * k))
+                               : make_float2(-INFINITY, 0.f);
+      mx = fmaxf(mx, s[k].x);
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 #pragma unroll
     for (int k = 0; k < kL; ++k) {
-      p[k] = p[k] == -INFINITY ? 0.f : exp2f(p[k] - mx);  // NaN stays
+      p[k] = s[k].x == -INFINITY ? -INFINITY : s[k].x - mx + s[k].y;
+      above = fmaxf(above, p[k]);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1)
+      above = fmaxf(above, __shfl_xor_sync(0xffffffffu, above, off));
+#pragma unroll
+    for (int k = 0; k < kL; ++k) {
+      p[k] = p[k] == -INFINITY ? 0.f : exp2f(p[k] - above);  // NaN stays
       l += p[k];
     }
 #pragma unroll
@@ -383,7 +395,7 @@ struct PgJoin {
   // Factor of the row's output; the first thread writes L.
   __device__ __forceinline__ float finish(const PagedArgs &a, bool first) const {
     const bool empty = mx == -INFINITY && l == 0.f;  // l may be NaN
-    const float L = empty ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
+    const float L = empty ? -INFINITY : (mx + (above + log2f(l))) * 0.69314718055994530942f;
     if (first) a.lse[orow] = L;
     return empty ? 0.f : sink_factor(a.sink, h, L) / l;
   }
@@ -442,7 +454,7 @@ PgLayout pg_layout(int n, int R) {
   L.joins = up((kPgMaxCtas + 1) * sizeof(int4));
   L.groups = L.joins + up((2 * kPgMaxCtas + 1) * sizeof(int4));
   L.lse = L.groups + up((size_t)n * sizeof(PgGroup));
-  L.o = L.lse + up((size_t)2 * kPgMaxCtas * R * 4);
+  L.o = L.lse + up((size_t)2 * kPgMaxCtas * R * sizeof(float2));
   L.total = L.o + (size_t)2 * kPgMaxCtas * R * CPMLA_DV * 4;
   return L;
 }
@@ -593,7 +605,7 @@ int paged_attn_args(const char *fn, bool four, const void *q, int64_t q_token_st
   a.start = reinterpret_cast<int4 *>(ws + L.start);
   a.joins = reinterpret_cast<int4 *>(ws + L.joins);
   a.groups = reinterpret_cast<PgGroup *>(ws + L.groups);
-  a.lse_part = reinterpret_cast<float *>(ws + L.lse);
+  a.lse_part = reinterpret_cast<float2 *>(ws + L.lse);
   a.o_part = reinterpret_cast<float *>(ws + L.o);
   *R_out = R;
   return CPMLA_OK;

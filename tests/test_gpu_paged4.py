@@ -546,6 +546,73 @@ def test_attn_scores_that_rise_and_fall(H):
         check_attn(d, b.values(), qg, o, lse, hi=[hi])
 
 
+def put_token(b, slot, e, lower=None, upper=None, rope=0):
+    """Token in a slot: exponent e, offsets 6 (values 2^e times the codes'), the E2M1 codes of
+    the words of channels 0-255 and 256-511 (None: zeros), all rope channels one E4M3 code."""
+    strip, r = b.cache.view(-1, 5392)[slot // 16], slot % 16
+    words = strip[256 * r:256 * r + 256].view(16, 2, 8)
+    words[:, 0] = 0 if lower is None else lower
+    words[:, 1] = 0 if upper is None else upper
+    strip[4096 + 64 * r:4160 + 64 * r] = rope
+    strip[5120 + 16 * r:5136 + 16 * r] = 0x66
+    strip[5376 + r] = 127 + e
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_attn_values_that_grow_by_more_than_binary32_holds(H):
+    """Three tiles of tokens of equal weight and of values 2^-64, 2^56 and 2^63 in size, the
+    last two in channels of their own (rows of 160 requests, so that many are one piece)."""
+    b = p4.Batch4([191] * 160, [1] * 160, 64, seed=93)
+    b.table[:] = b.table[0]
+    g = torch.Generator().manual_seed(94)
+    codes = lambda: torch.randint(0, 256, (16, 8), generator=g, dtype=torch.uint8)
+    for i, (e, low, up) in enumerate([(-64, 1, 1), (56, 1, 0), (63, 0, 1)]):
+        for r in range(64):
+            put_token(b, int(b.table[0, i]) * 64 + r, e, codes() if low else None,
+                      codes() if up else None)
+    d, q = b.gpu(), gpu(torch.zeros((160, H, 576)).bfloat16())
+    o, lse = run_attn(d, q)
+    check_attn(d, b.values(), q, o, lse)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("first", [-64, 119])
+def test_attn_tokens_at_both_ends_of_the_exponents(H, first):
+    """Zero tokens (e = -64) beside tokens at e = 119 with scores of the same size: the zero
+    ones have a good part of the weight, in tiles of their own and beside the others."""
+    b = p4.Batch4([191], [1], 64, seed=95)
+    g = torch.Generator().manual_seed(96)
+    codes = lambda: torch.randint(0, 256, (16, 8), generator=g, dtype=torch.uint8)
+    for p in range(192):
+        e = first if p // 64 == 0 or (p // 64 == 2 and p % 3) else 55 - first
+        slot = int(b.table[0, p // 64]) * 64 + p % 64
+        if e < 0:
+            put_token(b, slot, -64)
+        else:
+            put_token(b, slot, 119, codes(), codes(), 0x30 + p % 8)
+    d, q = b.gpu(), gpu(make_q(1, H, 97))
+    scale = SCALE * 2.0 ** -120
+    o, lse = run_attn(d, q, scale=scale)
+    check_attn(d, b.values(), q, o, lse, scale=scale)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_attn_scores_whose_last_bit_is_more_than_a_weights_range(H):
+    """Scores of 2^27 to 2^29 (binary32's step is 16 and more there): a third of the keys
+    have the largest, and the others nothing."""
+    b = p4.Batch4([319], [1], 64, seed=98)
+    g = torch.Generator().manual_seed(99)
+    codes = lambda: torch.randint(0, 256, (16, 8), generator=g, dtype=torch.uint8)
+    for p in range(320):
+        put_token(b, int(b.table[0, p // 64]) * 64 + p % 64, 0, codes(), codes(),
+                  0x78 if p % 3 == 0 else 0x70)      # 256 or 128
+    q = torch.zeros((1, H, 576))
+    q[0, :, 575] = 2.0 ** 23 * (1 + torch.arange(H) / 16)
+    d, q = b.gpu(), gpu(q.bfloat16())
+    o, lse = run_attn(d, q)
+    check_attn(d, b.values(), q, o, lse)
+
+
 @pytest.mark.parametrize("H", [16, 64])
 def test_attn_far_blocks(H):
     """Blocks whose bytes lie past 32 bits, and rows of q and o past them too."""
