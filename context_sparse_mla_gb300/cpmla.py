@@ -579,7 +579,8 @@ def mla_paged4_cache_read(cache, slot_mapping, *, out=None, stream=None):
     nb, bs, pc = _paged4(cache, dev)
     n = slot_mapping.numel()
     if out is None:
-        out = torch.empty((n, DQK), dtype=torch.bfloat16, device=cache.device)
+        with torch.cuda.stream(stream):  # whose work is ahead of the call may use the memory
+            out = torch.empty((n, DQK), dtype=torch.bfloat16, device=cache.device)
     p, st = _kv_rows(out, n, dev, "out")
     _launch((_lib or lib()).mla_paged4_cache_read, dev, stream, pc, nb, bs,
             _at(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, p, st)

@@ -249,6 +249,25 @@ def test_read(bs, n):
     assert cpmla.device_status() == 0
 
 
+def test_read_into_new_rows_of_another_stream():
+    """Rows that the call makes are of its stream's memory, not of memory that work queued
+    on the current stream may still use."""
+    cache = p4.random_cache(20, 64, 5)
+    slot = torch.randperm(1280, generator=torch.Generator().manual_seed(6))
+    want = p4.decode(cache.numpy()).reshape(-1, 576)[slot]
+    side, c, sl = torch.cuda.Stream(), gpu(cache), gpu(slot)
+    torch.cuda.synchronize()
+    busy = torch.full((1280, 576), 3.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(200):
+        busy.mul_(1.0)
+    at = busy.data_ptr()
+    del busy
+    out = cpmla.mla_paged4_cache_read(c, sl, stream=side)
+    assert out.data_ptr() != at
+    torch.cuda.synchronize()
+    assert np.array_equal(out.double().cpu().numpy(), want) and cpmla.device_status() == 0
+
+
 def test_slots_outside_are_skipped_and_recorded():
     kv = rows(6, 3)
     cache = torch.randint(0, 256, (2, 1, 5392), dtype=torch.uint8)
