@@ -15,19 +15,20 @@
 // E5M2 (a range for a whole tile) take 24.
 //
 // A piece of work is R = 16 or 64 rows (tokens of one request x heads) and a range of their
-// keys, as the plan cuts them.  Warps: 0-2 issue the MMAs, 3 loads, 4-11 do the softmax and
+// keys, as the plan cuts them.  Warps: 0 and 1 (R = 16: 2 too)
+// issue the MMAs, 3 loads, 4-11 do the softmax and
 // the output, 12-15 bring q in, 16-23 expand.  Every wait is bounded; on expiry the CTA
 // records CPMLA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 //
 // What bounds it, measured (32 tokens of 4,096 to 131,072 keys).  R = 16: 184 us a call
-// with 16 heads, 3.6 TB/s (the 8-bit cache's 212, 5.2 TB/s); R = 64: 266 us with 64 heads,
-// 1.04 PFLOP/s of the exact products (270).  A tile takes 1,700 and 2,450 cycles.  Shared
+// with 16 heads, 3.6 TB/s (the 8-bit cache's 212, 5.2 TB/s); R = 64: 260 us with 64 heads,
+// 1.06 PFLOP/s of the exact products (270).  A tile takes 1,700 and 2,400 cycles.  Shared
 // memory is busy for 1,300 and 1,900 of them, the tensor core for 800 and 1,300, and a
 // scheduler issues 1,250 and 1,550 instructions, half of them of the pipe that takes one
 // every two cycles (the expansion alone 730 cycles).  None of these fills the time: a tile
 // keeps its place in the ring for the chain of its expansion, scores, softmax and PV, 8,300
 // and 9,700 cycles, and there are places for 5 and 4.  8,192 prompt tokens of 16 heads
-// 1,200 us (1,160).  On the way here: the roles' loops have to fit the instruction cache
+// 1,175 us (1,160).  On the way here: the roles' loops have to fit the instruction cache
 // together (a softmax loop with 32 keys side by side instead of 16: 680 us for the 64
 // heads); a wait by one lane leaves its warp apart, and what follows is issued twice (484,
 // 398); a tile's MMAs behind one election (266, 325 with one for each); a reference that
@@ -57,9 +58,10 @@ struct P4Cfg {
   // R = 16: both parts of P side by side in one PV MMA, with accumulators of their own
   static constexpr int kWide = R == 16 ? 2 : 1;
   static constexpr int kOW = R * kWide;  // columns of an O^T chunk
-  // MMA issuers (warps 0-2): R = 64 has 16 PV MMAs a tile for two warps beside the 18 of
-  // the scores, R = 16 has 8 for one, and the scores two
-  static constexpr int kPvW = R == 64 ? 2 : 1, kQkW = 3 - kPvW;
+  // Issuers of the scores: with 16 rows two, for the even and the odd tiles (184 us for 32
+  // tokens of 16 heads, 189 with one); with 64 rows one (260 us with 64 heads, 266 with two
+  // for PV beside it).
+  static constexpr int kQkW = R == 64 ? 1 : 2;
   // R = 16: q lies in each quarter of the lanes, so that any warp has the scores of all
   // rows: two of a softmax warpgroup take 32 of the tile's keys each, others than the
   // other warpgroup's, so that every scheduler has one (189 us for the 32 tokens of 16
@@ -67,15 +69,15 @@ struct P4Cfg {
   static constexpr bool kSplit = R == 16;
   static constexpr int kLanes = kSplit ? 2 * R : R;  // rows and their copies
   static constexpr int kLive = kLanes / 16;          // warps of a warpgroup that have rows
-  // q's steps of 32 channels in TMEM (64 rows leave columns for 14), and the rest in
+  // q's steps of 32 channels in TMEM (64 rows leave columns for 15; an even number is less code), and the rest in
   // shared memory: [2R lanes x 64] a pair of steps
   static constexpr int kQSteps = R == 64 ? 14 : 18;
   static constexpr int kQPair = 2 * R * 64, kQRest = (18 - kQSteps) / 2 * kQPair;
-  // TMEM columns behind q's: the scales of the values (1, four columns) and of the
-  // weights, for each PV issuer (four; rows 32 x .. 32 x + 31 in column x, in each quarter
-  // of the lanes); two S buffers; O^T
+  // TMEM columns behind q's: the scales of the values (1, four columns) and of the weights
+  // (four; rows 32 x .. 32 x + 31 in column x, in each quarter of the lanes); two S
+  // buffers; O^T
   static constexpr int kColScale = 8 * kQSteps;
-  static constexpr int kColS = (kColScale + 12 + 15) / 16 * 16;
+  static constexpr int kColS = (kColScale + 8 + 15) / 16 * 16;
   static constexpr int kColO = kColS + 2 * kPgTile;
   static_assert(kColO + 4 * kOW <= (int)kPgTmemCols, "TMEM columns");
   // places for tiles, for the strips that are expanded into them, and for the tiles' rope,
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&c.full[s], 4);
-      mbar_init(&c.empty[s], Cfg::kPvW);
+      mbar_init(&c.empty[s], 1);
     }
     for (int s = 0; s < NP; ++s) {
       mbar_init(&c.pack_full[s], 1);
@@ -259,13 +261,13 @@ __global__ void __launch_bounds__(kP4Threads, 1)
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.s_free[s], Cfg::kLive);
       mbar_init(&c.p_full[s], Cfg::kLive);
-      mbar_init(&c.p_free[s], Cfg::kPvW);
+      mbar_init(&c.p_free[s], 1);
       mbar_init(&c.q_full[s], 4);
       mbar_init(&c.o_free[s], 8);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&c.ref[s], 1);
     mbar_init(&c.q_free, Cfg::kQkW);
-    mbar_init(&c.o_full, Cfg::kPvW);
+    mbar_init(&c.o_full, 1);
     for (int s = 0; s < 3; ++s) mbar_init(&c.drain[s], 1);
     c.abort = 0;
     fence_mbar_init();
@@ -332,9 +334,8 @@ __global__ void __launch_bounds__(kP4Threads, 1)
         pg_drain(&c.drain[warp], 0, kWaitLimitNs);
       }
       __syncwarp();
-    } else if (warp < 3) {
-      // ------------------------------------------------------ PV-GEMM issuers
-      const int me = warp - 1;
+    } else if (warp == 1) {
+      // ------------------------------------------------------ PV-GEMM issuer
       constexpr int W = Cfg::kWide;  // parts a MMA
       constexpr uint32_t id = idesc_mx_e4m3(128, R * W, 1, 0);
       const uint64_t dp = smem_desc(smem_u32(sP), 16, 512, kSwz64);
@@ -354,10 +355,9 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           tc_fence_after();
           if (elect_one()) {
             // (the scales of the tile before are read: a thread's copies and MMAs are in order)
-            tmem_cp_32x128b(tSB + 4 * me, df + ((b * sizeof c.sf[0]) >> 4));
+            tmem_cp_32x128b(tSB, df + ((b * sizeof c.sf[0]) >> 4));
 #pragma unroll
-            for (int cx = 0; cx < 4 / Cfg::kPvW; ++cx) {
-              const int ch = me + Cfg::kPvW * cx;
+            for (int ch = 0; ch < 4; ++ch) {
               const uint64_t da = dr + ((j % NS * kP4Tile + ch * kPgSlot) >> 4);
               uint32_t acc = t > w.t0 ? 1u : 0u;
 #pragma unroll
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
                   const uint64_t db = dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4);
                   // (a byte of a row's scales for each 32 keys)
                   mma_mx_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4), db,
-                            id | idesc_mx_b_scale(k), tSA, tSB + 4 * me, acc);
+                            id | idesc_mx_b_scale(k), tSA, tSB, acc);
                   acc = 1;
                 }
             }
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
         pg_drain(&c.drain[warp], 0, kWaitLimitNs);
       }
       __syncwarp();
-    } else {
+    } else if (warp == 3) {
       // ------------------------------------------------------ loads
       // Lane p: page p of a tile (a tile is half of a block of 128), whose strips lie side
       // by side: one copy.
