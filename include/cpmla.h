@@ -667,6 +667,9 @@ int mla_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int H
  * mla_paged4_attn -- mla_paged_attn over this cache: arguments, results, workspace
  * (mla_paged_attn_workspace_size) and errors as there, without cache_exp.  What
  * lies in the cache at positions that a row does not attend to does not reach it.
+ * A key whose token's scale is 2^-183 of another's that the row attends to (the two
+ * ends of the format) and whose weight is below 2^-23 of that one's may be left out
+ * of the softmax sum.
  *
  * All three: nothing is allocated, no host synchronisation, usable in stream
  * capture.  Errors: CPMLA_ERR_ARG, CPMLA_ERR_UNSUPPORTED, CPMLA_ERR_CUDA.
