@@ -560,7 +560,10 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           if (lane == 0) c.mv[wg][q4] = mv;
           named_bar_sync(bar_wg, 128);
           if ((c.mv[wg][0] | c.mv[wg][1] | c.mv[wg][2] | c.mv[wg][3]) != 0) {
-            // the PV GEMM of the tile before is done with O^T
+            // the PV GEMM of the tile before is done with O^T; behind that of the one ahead of
+            // it, as a wait tells a phase from the next alone (jj - 3 may still run)
+            if (ok && jj >= 2)
+              ok = warp_wait(&c.p_free[wg], ((jj >> 1) - 1) & 1, abort, a.status);
             if (ok)
               ok = warp_wait(&c.p_free[wg ^ 1], ((jj - 1) >> 1) & 1, abort, a.status);
             tc_fence_after();

@@ -540,7 +540,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             c.alpha[wg][r] = m_old == -INFINITY ? 0.f : fast_exp2(m_old - m_new);
           if (lane == 0) c.mv[wg][q4] = mv;
           named_bar_sync(bar_wg, 128);
-          // the PV GEMM of the tile before is done with O^T
+          // the PV GEMM of the tile before is done with O^T; behind that of the one ahead of
+          // it, as a wait tells a phase from the next alone (jj - 3 may still run)
+          if (ok && jj >= 2)
+            ok = warp_wait(&c.p_free[wg], ((jj >> 1) - 1) & 1, lane, abort, a.status);
           if (ok) ok = warp_wait(&c.p_free[wg ^ 1], ((jj - 1) >> 1) & 1, lane, abort, a.status);
           tc_fence_after();
           if (ok) {
