@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kP4Threads, 1)
       const float qf = ok && some && mine ? c.qf[piece & 1][r] : 0.f;
       float m_own = -INFINITY, l = 0.f;  // the sum l of 2^t is on reference m_own
       for (uint32_t jj = j + (x - w.t0); x < w.t1; x += 2, jj += 2) {
-        if (ok) ok = warp_wait(&c.s_full[wg], (jj >> 1) & 1, abort, a.status);
+        // (warps that free the scores alone: for others the next ones may be there already)
+        if (live && ok) ok = warp_wait(&c.s_full[wg], (jj >> 1) & 1, abort, a.status);
         tc_fence_after();
         // Steps of kK keys a thread, rolled: the roles' loops have to stay in the
         // instruction cache together (32 KB at an instruction a cycle).  Between the

@@ -139,7 +139,8 @@ class Model:
                 if j % 2 != wg:
                     continue
                 first, move = j == tiles[0], j > tiles[0] and self.moves[j]
-                yield self.s_full[wg], j >> 1
+                if live or "scores for all warps" in self.planted:
+                    yield self.s_full[wg], j >> 1
                 if live:
                     self.s_free[wg].arrive()
                 if live and not first:
@@ -212,7 +213,7 @@ class Model:
                         step(a)
                     except StopIteration:
                         left.discard(a)
-                if idle > 200000:
+                if idle > 20000:
                     raise Fault("no agent goes on")
 
 
@@ -227,11 +228,14 @@ def test_waits_pass_on_their_own_phase(four, rows):
 
 
 @pytest.mark.parametrize("four, rows, planted, word", [
+    (True, 16, "rescale behind one phase", "two before|under the PV"),
     (True, 64, "rescale behind one phase", "two before|under the PV"),
     (False, 16, "rescale behind one phase", "two before|under the PV"),
     (False, 64, "rescale behind one phase", "two before|under the PV"),
+    (True, 16, "scores for all warps", "over|no agent"),
 ])
 def test_the_model_finds(four, rows, planted, word):
-    """Orders that the kernels do not have: a rescale that waits for the last tile alone."""
+    """Orders that the kernels do not have: a rescale that waits for the last tile alone,
+    warps that wait for scores which others free."""
     with pytest.raises(Fault, match=word):
         runs(four, rows, 400, (planted,))
