@@ -974,10 +974,18 @@ __global__ void __launch_bounds__(kP4Threads, 1)
         const int e = strip[kStripExp + u];
         const uint32_t there = c.there[ps];
         warp_arrive(&c.pack_empty[ps], lane);
-        // (two waits at once: the PV GEMM is done with the tile's place, the scores with
-        // the rope's; a barrier's phase before its first is complete)
-        ok = warp_wait(half ? &c.rope_free[j % NR] : &c.empty[es],
-                       ((half ? j / NR : j / NS) & 1) ^ 1, abort, a.status);
+        // The PV GEMM is done with the tile's place, the scores with the rope's (a barrier's
+        // phase before its first is complete).  The rope's phase ahead of this one, tile j -
+        // 6's, has to be over before that wait: with one issuer, whose scores end in order,
+        // this group's last one was for j - 5's, and the two are waited for at once; with two
+        // issuers the tile's place tells it (j - 5's values are behind j - 6's scores).
+        if constexpr (Cfg::kQkW == 1) {
+          ok = warp_wait(half ? &c.rope_free[j % NR] : &c.empty[es],
+                         ((half ? j / NR : j / NS) & 1) ^ 1, abort, a.status);
+        } else {
+          ok = warp_wait(&c.empty[es], (j / NS & 1) ^ 1, abort, a.status);
+          if (ok) ok = warp_wait(&c.rope_free[j % NR], (j / NR & 1) ^ 1, abort, a.status);
+        }
         if (!ok) break;
         uint8_t *dst = sRing + es * kP4Tile + (u >> 3) * kPgSlot + (k0 + half) * 128;
         // (four tokens a turn: 8,192 prompt tokens 1,197 us, 1,220 with all eight side by side)

@@ -81,8 +81,12 @@ class Model:
                 self.pack_empty[j % NP].arrive()
                 place, rope = (self.empty[j % self.ns], j // self.ns - 1), \
                     (self.rope_free[j % NR], j // NR - 1)
-                yield rope  # lanes of one warp wait for either, in any order
-                yield place
+                if self.qk == 1 or "rope beside place" in self.planted:
+                    yield rope  # lanes of one warp wait for either, in any order
+                    yield place
+                else:
+                    yield place
+                    yield rope
                 self.full[j % self.ns].arrive()
 
     def scores(self, me, q):
@@ -222,7 +226,8 @@ def runs(four, rows, n, planted=()):
         Model(four, rows, random.Random(seed), planted).run()
 
 
-@pytest.mark.parametrize("four, rows", [(True, 64), (False, 16), (False, 64)])
+@pytest.mark.parametrize("rows", [16, 64])
+@pytest.mark.parametrize("four", [True, False])
 def test_waits_pass_on_their_own_phase(four, rows):
     runs(four, rows, 300)
 
@@ -233,9 +238,11 @@ def test_waits_pass_on_their_own_phase(four, rows):
     (False, 16, "rescale behind one phase", "two before|under the PV"),
     (False, 64, "rescale behind one phase", "two before|under the PV"),
     (True, 16, "scores for all warps", "over|no agent"),
+    (True, 16, "rope beside place", "two before"),
 ])
 def test_the_model_finds(four, rows, planted, word):
     """Orders that the kernels do not have: a rescale that waits for the last tile alone,
-    warps that wait for scores which others free."""
+    warps that wait for scores which others free, a place for the rope waited for beside
+    the one in the ring."""
     with pytest.raises(Fault, match=word):
         runs(four, rows, 400, (planted,))
