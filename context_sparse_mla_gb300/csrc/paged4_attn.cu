@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
       if (mine) {
         const int i = w.m.first + r / a.hc;
         lo = a.kv_lo ? max(a.kv_lo[i], 0) : 0;
-        hi = a.kv_hi ? min(a.kv_hi[i], a.pos[i]) : a.pos[i];
+        hi = a.kv_hi ? max(-1, min(a.kv_hi[i], a.pos[i])) : a.pos[i];  // (p4_rare subtracts)
       }
       x = w.t0 + ((j & 1) == (uint32_t)wg ? 0 : 1);  // this warpgroup's first tile
     };

@@ -672,6 +672,33 @@ def test_attn_blocks_that_no_row_attends_to_may_be_anything(H):
         cpmla.device_status(clear=True)
 
 
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("H", [4, 16, 64])
+def test_attn_bounds_at_the_ends_of_int32(H, tall):
+    """Bounds of -2^31 and 2^31 - 1 beside ordinary ones in the same pieces (tall: in a table
+    of as many rows as there are entries, which makes them pieces of 16 rows): those that
+    leave no key see none, and the others have the bits that bounds next to the keys give."""
+    ctx, new = [600, 0, 90, 300], [70, 33, 1, 9]
+    b = p4.Batch4(ctx, new, 32, seed=101)
+    n = len(b.pos)
+    if tall:
+        b.table = np.concatenate([b.table, np.full((n, b.table.shape[1]), -1, np.int32)])
+    least, most = -2 ** 31, 2 ** 31 - 1
+    i = np.arange(n)
+    lo, hi = np.where(i % 3 == 1, 40, 0), b.pos.astype(np.int64)
+    near = np.where(i % 5 == 2, -1, hi), np.where(i % 7 == 3, b.pos + 1, lo)
+    far = np.where(i % 5 == 2, least, np.where(i % 2 == 1, most, hi)), \
+        np.where(i % 7 == 3, most, np.where(lo == 0, least, lo))
+    d, q, val = b.gpu(), gpu(make_q(n, H, 102)), b.values()
+    o, lse = run_attn(d, q, lo=far[1], hi=far[0], fill=7.0)
+    check_attn(d, val, q, o, lse, lo=far[1], hi=far[0])
+    none = np.maximum(far[1], 0) > np.minimum(far[0], b.pos)
+    assert none[i % 5 == 2].all() and none[i % 7 == 3].all()
+    assert (o[none] == 0).all() and torch.isneginf(lse[none]).all()
+    o2, lse2 = run_attn(d, q, lo=near[1], hi=near[0], fill=7.0)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_attn_lists_of_padding_only():
     z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")
     table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
