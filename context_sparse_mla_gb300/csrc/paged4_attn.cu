@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           const bool some_key = mine && bt > -INFINITY;
           // (from 2^27 on the difference is rounded, to 16 too, which an E4M3 does not hold)
           const float top = bt - (ceilf(bt) - 8.f) > 8.f ? bt : ceilf(bt) - 8.f;
-          const float sub = some_key ? fmaxf(top, m_new - 120.f) : 0.f;
+          // (rounded up: to nearest it may be 128 below m, and the scale's byte that of NaN)
+          const float sub = some_key ? fmaxf(top, __fadd_ru(m_new, -120.f)) : 0.f;
           // the PV GEMM of this buffer's last tile is done with it
           if (ok && jj >= 2)
             ok = warp_wait(&c.p_free[wg], ((jj >> 1) - 1) & 1, abort, a.status);

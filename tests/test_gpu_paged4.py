@@ -632,6 +632,27 @@ def test_attn_scores_whose_last_bit_is_more_than_a_weights_range(H):
     check_attn(d, b.values(), q, o, lse)
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("top", [[5], [200, 300], list(range(64, 96))])
+@pytest.mark.parametrize("binade", range(6))
+@pytest.mark.parametrize("H", [16, 64])
+def test_attn_large_scores_at_few_keys(H, binade, top, sign):
+    """Scores of 2^26 to 2^32 and of their half, the larger (of both signs) at few keys: whole
+    tiles, and whole sets of the 32 keys that share a scale, lie far below the reference,
+    where binary32's step is 8 to 256."""
+    b = p4.Batch4([319], [1], 64, seed=103)
+    g = torch.Generator().manual_seed(104)
+    codes = lambda: torch.randint(0, 256, (16, 8), generator=g, dtype=torch.uint8)
+    for p in range(320):
+        put_token(b, int(b.table[0, p // 64]) * 64 + p % 64, 0, codes(), codes(),
+                  0x78 if (p in top) == (sign > 0) else 0x70)      # 256 or 128
+    q = torch.zeros((1, H, 576))
+    q[0, :, 575] = sign * 2.0 ** (22 + binade) * (1 + torch.arange(H) % 16 / 16)
+    d, q = b.gpu(), gpu(q.bfloat16())
+    o, lse = run_attn(d, q)
+    check_attn(d, b.values(), q, o, lse)
+
+
 @pytest.mark.parametrize("H", [16, 64])
 def test_attn_far_blocks(H):
     """Blocks whose bytes lie past 32 bits, and rows of q and o past them too."""
