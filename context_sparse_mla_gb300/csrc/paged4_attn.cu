@@ -212,8 +212,8 @@ __device__ __noinline__ float p4_rare(float *u, const float *e, int n, int p, in
     }
   }
   u[n + 2] = wide ? 1.f : 0.f;
+  u[n] = t_max;  // (-inf, no reference at all, where nothing is left)
   if (t_max == -INFINITY) t_max = 0.f;
-  u[n] = t_max;
   if (__any_sync(0xffffffffu, wide))
 #pragma unroll 4
     for (int i = 0; i < n; ++i) t_sum += fast_exp2(u[i] - e[i] - t_max);

@@ -653,6 +653,51 @@ def test_attn_large_scores_at_few_keys(H, binade, top, sign):
     check_attn(d, b.values(), q, o, lse)
 
 
+@pytest.mark.parametrize("far", [-1000, 0, 1000])
+@pytest.mark.parametrize("H", [1, 16, 64])
+def test_attn_large_tokens_in_tiles_that_are_cut(H, far):
+    """Tokens at e = 30 whose scores all lie about `far` (base 2), in rows whose first and last
+    keys are anywhere in a tile: a thread's share of it may have none."""
+    hi = [0, 5, 15, 16, 31, 40, 47, 63, 64, 79, 130, 175] + [100] * 6 + [191]
+    lo = [0] * 12 + [1, 16, 20, 48, 70, 99] + [177]
+    n = len(hi)
+    b = p4.Batch4([191], [1], 64, seed=105)
+    g = torch.Generator().manual_seed(106)
+    codes = lambda: torch.randint(0, 256, (16, 8), generator=g, dtype=torch.uint8)
+    for p in range(192):
+        put_token(b, int(b.table[0, p // 64]) * 64 + p % 64, 30, codes(), codes(), 0x38)  # 1
+    b.table = np.repeat(b.table, n, 0)
+    b.pos, b.req = np.full(n, 191, np.int32), np.arange(n, dtype=np.int32)
+    q = make_q(n, H, 107)
+    q[..., 512:] = 0
+    q[..., 575] = far * 16  # x 1 / 24 x log2 e: 0.96 far
+    scale = SCALE * 2.0 ** -30
+    d, q, val = b.gpu(), gpu(q), b.values()
+    o, lse = run_attn(d, q, lo=lo, hi=hi, scale=scale)
+    # check_attn's bounds, and what a row of q loses in two E4M3 where one channel is 16,000
+    # times the others: with its largest in (224, 448] units a channel is held to 2^-14 of one
+    # (half of the second E4M3's least step, 2^-9 / 16), so a score is off by at most `off` =
+    # 2^-14 units x the token's sum of |values| x scale; the sum of weights by e^off, a
+    # weight by e^(2 off).  (Found to be needed: 1.4e-2 of the 0.2 that this is.)
+    unit = torch.exp2(torch.ceil(torch.log2(q.double().abs().amax(2) / 448)))
+    off = 2.0 ** -14 * unit * val[b.table[0, :3].tolist()].abs().sum(-1).max() * scale
+    tok, pos, req = range(n), d["pos"].cpu().numpy(), d["req"].cpu().numpy()
+    ref = p4.attend(q, val, d["cache"], d["block_table"], tok, pos, req, scale, None, lo, hi)
+    for i, (ro, rl, w, wt) in ref.items():
+        dl, x = (lse[i].double() - rl).abs(), off[i]
+        assert (dl <= LSE_ABS + LSE_REL * rl.abs() + x).all(), (i, float(dl.max()))
+        do, x = (o[i].double() - ro).abs(), torch.expm1(2 * off[i])[:, None]
+        assert (do <= O_REL * ro.abs() + (O_WEIGHT + x) * w + O_TILE * wt + 1e-30).all(), i
+    assert cpmla.device_status() == 0
+    # a thread's only key is NaN
+    s = int(b.table[0, 0]) * 64 + 16
+    b.cache.view(-1, 5392)[s // 16, 5376 + s % 16] = 255
+    o2, lse2 = run_attn(b.gpu(), q, lo=lo, hi=hi, scale=scale)
+    sees = gpu(np.array([a <= 16 <= z for a, z in zip(lo, hi)]))
+    assert lse2[sees].isnan().all() and o2[sees].isnan().all()
+    assert torch.equal(o[~sees], o2[~sees]) and torch.equal(lse[~sees], lse2[~sees])
+
+
 @pytest.mark.parametrize("H", [16, 64])
 def test_attn_far_blocks(H):
     """Blocks whose bytes lie past 32 bits, and rows of q and o past them too."""
