@@ -20,15 +20,15 @@
 // the output, 12-15 bring q in, 16-23 expand.  Every wait is bounded; on expiry the CTA
 // records CPMLA_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 //
-// What bounds it, measured (32 tokens of 4,096 to 131,072 keys).  R = 16: 184 us a call
-// with 16 heads, 3.6 TB/s (the 8-bit cache's 212, 5.2 TB/s); R = 64: 260 us with 64 heads,
-// 1.06 PFLOP/s of the exact products (270).  A tile takes 1,700 and 2,400 cycles.  Shared
+// What bounds it, measured (32 tokens of 4,096 to 131,072 keys).  R = 16: 185 us a call
+// with 16 heads, 3.6 TB/s (the 8-bit cache's 222, 5.1 TB/s); R = 64: 266 us with 64 heads,
+// 1.04 PFLOP/s of the exact products (271).  A tile takes 1,700 and 2,500 cycles.  Shared
 // memory is busy for 1,300 and 1,900 of them, the tensor core for 800 and 1,300, and a
 // scheduler issues 1,250 and 1,550 instructions, half of them of the pipe that takes one
 // every two cycles (the expansion alone 730 cycles).  None of these fills the time: a tile
 // keeps its place in the ring for the chain of its expansion, scores, softmax and PV, 8,300
 // and 9,700 cycles, and there are places for 5 and 4.  8,192 prompt tokens of 16 heads
-// 1,175 us (1,160).  On the way here: the roles' loops have to fit the instruction cache
+// 1,184 us (1,151).  On the way here: the roles' loops have to fit the instruction cache
 // together (a softmax loop with 32 keys side by side instead of 16: 680 us for the 64
 // heads); a wait by one lane leaves its warp apart, and what follows is issued twice (484,
 // 398); a tile's MMAs behind one election (266, 325 with one for each); a reference that
@@ -69,8 +69,8 @@ struct P4Cfg {
   static constexpr bool kSplit = R == 16;
   static constexpr int kLanes = kSplit ? 2 * R : R;  // rows and their copies
   static constexpr int kLive = kLanes / 16;          // warps of a warpgroup that have rows
-  // q's steps of 32 channels in TMEM (64 rows leave columns for 15; an even number is less code), and the rest in
-  // shared memory: [2R lanes x 64] a pair of steps
+  // q's steps of 32 channels in TMEM (64 rows leave columns for 15; an even number is less
+  // code), and the rest in shared memory: [2R lanes x 64] a pair of steps
   static constexpr int kQSteps = R == 64 ? 14 : 18;
   static constexpr int kQPair = 2 * R * 64, kQRest = (18 - kQSteps) / 2 * kQPair;
   // TMEM columns behind q's: the scales of the values (1, four columns) and of the weights
@@ -180,8 +180,9 @@ __device__ __forceinline__ uint2 split_p4(uint32_t x, uint32_t y) {
 // Weights have scales of their own and the sum of 2^t has a reference of its own,
 // so that only O^T limits m: a row's m starts kP4Over above its first tile's largest u and
 // moves when a tile's largest lies kP4Up above it; a sum of 2^30 values stays below
-// 2^(30 + 9 + 80), and of a tile that lies so far below that its weights lose bits (72
-// under the first) nothing reaches binary32.  m never goes down.  (With m 6 below the first
+// 2^(30 + 9 + 80).  A tile's weights lose bits where its largest u lies 72 below the first
+// tile's, and are 0 at 89: in a channel that the heavier tokens have, binary32 holds
+// nothing of them either; in one where those are all zero they are lost.  m never goes down.  (With m 6 below the first
 // tile's largest and moves 28 above it each row moves now and then, and every eighth tile
 // of 64 rows waits for the PV GEMM: 394 us where this takes 257.)
 constexpr float kP4Over = 40.f, kP4Up = 80.f;
@@ -528,7 +529,8 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           if (((there ^ 15u) | th.y) != 0 || p0 < w.m.lo_max || p0 + kPgTile - 1 > w.m.hi_min) {
 #pragma unroll
             for (int n = 0; n < kU; ++n) rare[n] = u[n];
-            bt = p4_rare(rare, ks.e + p4_key(kb), kU, p0 + kb, lo, hi, there >> (kb >> 4), a.status);
+            bt = p4_rare(rare, ks.e + p4_key(kb), kU, p0 + kb, lo, hi, there >> (kb >> 4),
+                         a.status);
 #pragma unroll
             for (int n = 0; n < kU; ++n) u[n] = rare[n];
             if (kSplit) rare[kU + 2] += __shfl_xor_sync(0xffffffffu, rare[kU + 2], 16);

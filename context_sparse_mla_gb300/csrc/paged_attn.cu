@@ -49,7 +49,7 @@
 // its copies and MMAs, frees TMEM and exits.
 //
 // What bounds it, measured.  R = 16 (32 tokens of 4,096 to 131,072 keys x 16 heads):
-// HBM; 219 us a call, 5.2 TB/s over the whole call, 5.6 in the kernel.  R = 64: shared
+// HBM; 222 us a call, 5.1 TB/s over the whole call, 5.6 in the kernel.  R = 64: shared
 // memory and the MMA issue.  A tile's 42 MMAs read 188 KB of it (each part of p
 // reads the 4 KB of keys again: three parts side by side would need 768 TMEM
 // columns) and the copies write 36 KB, about 1,800 cycles at 128 B a cycle; it

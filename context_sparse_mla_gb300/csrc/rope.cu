@@ -4,7 +4,9 @@
 // The angle pos * f has to be known modulo a turn, and pos is large: in units of 2^-64
 // of a turn, with f as a whole number F of them, pos * F modulo 2^64 is exact, so one
 // 64-bit product replaces a reduction in binary64 (of which a GB300 does few).  F is
-// off by half a unit: 2^-34 of a turn at the largest position.
+// off by less than 5/4 units (f below 2^-9 has bits behind the last, which are cut):
+// 2^-32 of a turn at the largest position.  The half turns that are left, in [-1, 1), are
+// rounded to binary32: by 2^-26 of a turn, 1e-7, at most.
 //
 // A row is 128 B in a longer one.  8 lanes take a row, 4 rows a step of a warp; lane
 // 8 i + c computes pair 4 c + i, and the lanes of a column c share theirs: each needs

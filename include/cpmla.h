@@ -590,8 +590,9 @@ int mla_paged_attn(const void *q, int64_t q_token_stride, int H, const void *cac
  * (x[2i], x[2i+1]) (CPMLA_ROPE_PAIRS) or (x[i], x[i+32]) (CPMLA_ROPE_HALVES)
  *   (u', v') = amplitude * (u cos - v sin, u sin + v cos)
  * in binary32, rounded once to bf16, at the same places of the output; inverse
- * != 0 negates the angles (which is also the gradient of the rotation, or takes
- * it back).  The angle is exact modulo a turn to 2^-33 turns at every position.
+ * != 0 negates the angles (with the same amplitude that is the gradient of the
+ * rotation, with 1 / amplitude it takes it back).  At every position the angle modulo
+ * a turn is what binary32 holds of it: off by at most 2^-26 of a turn, and 2^-32.
  *   q, q_out     bf16; entry t's head h at q + t * q_token_stride + h *
  *                q_head_stride (elements, host), 64 channels side by side; NULL
  *                with H = 0.  Views into wider rows are usual: the last 64 of a
@@ -610,7 +611,8 @@ int mla_paged_attn(const void *q, int64_t q_token_stride, int H, const void *cac
  * mla_rope_freqs (host): inv_freq[i] = f_i = base^(-2i/64) for factor == 1, else
  * those of the "YaRN" scaling (Peng et al. 2023): with turns(b) = 64
  * ln(original_len / (2 pi b)) / (2 ln base), lo = max(0, floor(turns(beta_fast))),
- * hi = min(63, ceil(turns(beta_slow))) and r = clamp((i - lo) / (hi - lo), 0, 1),
+ * hi = min(63, ceil(turns(beta_slow))) and r = clamp((i - lo) / w, 0, 1), w = hi - lo
+ * or 1/1000 if that is less,
  *   inv_freq[i] = f_i (1 - r) + f_i / factor * r
  *   base > 1, factor >= 1; original_len >= 1 and 0 < beta_slow < beta_fast when
  *   factor > 1 (32 and 1 are usual)
@@ -667,9 +669,17 @@ int mla_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int H
  * mla_paged4_attn -- mla_paged_attn over this cache: arguments, results, workspace
  * (mla_paged_attn_workspace_size) and errors as there, without cache_exp.  What
  * lies in the cache at positions that a row does not attend to does not reach it.
- * A key whose token's scale is 2^-183 of another's that the row attends to (the two
- * ends of the format) and whose weight is below 2^-23 of that one's may be left out
- * of the softmax sum.
+ * Rounding: q is held to 8 significant bits, and no further than to 2^-21 of its row's
+ * largest channel.  A key's weight times its token's scale 2^e is held to 8 significant
+ * bits, and no further than to 2^-17 of the largest such product of the 32 keys at
+ * positions 32 i .. 32 i + 31, and to 2^-89 of the row's: a channel that is zero in all
+ * heavier tokens loses what lies below (of all real caches, nothing).  The softmax sum
+ * does not go by these bits; a key whose token's scale is 2^-183 of another's that the
+ * row attends to (the two ends of the format) and whose weight is below 2^-22 of that
+ * one's may be left out of it.  Scores are binary32.
+ * It is the faster one where reading the cache bounds a step (single tokens, few heads);
+ * prompts take up to 3% longer than with 8 bits, as their tiles are expanded anew for
+ * each piece that reads them.
  *
  * All three: nothing is allocated, no host synchronisation, usable in stream
  * capture.  Errors: CPMLA_ERR_ARG, CPMLA_ERR_UNSUPPORTED, CPMLA_ERR_CUDA.
