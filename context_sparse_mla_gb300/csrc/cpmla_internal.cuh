@@ -280,7 +280,8 @@ __device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 // 32 rows of 16 bytes, side by side in shared memory, to four columns of each quarter of
-// the lanes; in order with the issuing thread's MMAs.
+// the lanes; ahead of the issuing thread's later MMAs (and not known to be behind its
+// earlier ones).
 __device__ __forceinline__ void tmem_cp_32x128b(uint32_t d_tmem, uint64_t s_desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(s_desc)
                : "memory");

@@ -74,10 +74,10 @@ struct P4Cfg {
   static constexpr int kQSteps = R == 64 ? 14 : 18;
   static constexpr int kQPair = 2 * R * 64, kQRest = (18 - kQSteps) / 2 * kQPair;
   // TMEM columns behind q's: the scales of the values (1, four columns) and of the weights
-  // (four; rows 32 x .. 32 x + 31 in column x, in each quarter of the lanes); two S
-  // buffers; O^T
+  // (four for even and for odd tiles; rows 32 x .. 32 x + 31 in column x, in each quarter
+  // of the lanes); two S buffers; O^T
   static constexpr int kColScale = 8 * kQSteps;
-  static constexpr int kColS = (kColScale + 8 + 15) / 16 * 16;
+  static constexpr int kColS = (kColScale + 12 + 15) / 16 * 16;
   static constexpr int kColO = kColS + 2 * kPgTile;
   static_assert(kColO + 4 * kOW <= (int)kPgTmemCols, "TMEM columns");
   // places for tiles, for the strips that are expanded into them, and for the tiles' rope,
@@ -355,8 +355,10 @@ __global__ void __launch_bounds__(kP4Threads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            // (the scales of the tile before are read: a thread's copies and MMAs are in order)
-            tmem_cp_32x128b(tSB, df + ((b * sizeof c.sf[0]) >> 4));
+            // (a thread's MMAs are behind its copies, but a copy need not be behind MMAs: the
+            // scales of the tile before have a place of their own, and those of the one ahead of
+            // it are read, as this tile's weights are only there behind its PV GEMM)
+            tmem_cp_32x128b(tSB + 4 * b, df + ((b * sizeof c.sf[0]) >> 4));
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
               const uint64_t da = dr + ((j % NS * kP4Tile + ch * kPgSlot) >> 4);
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kP4Threads, 1)
                   const uint64_t db = dp + ((b * Cfg::kP + y * Cfg::kPart + k * 32) >> 4);
                   // (a byte of a row's scales for each 32 keys)
                   mma_mx_ss(tO + ch * Cfg::kOW, da + ((k * 4096) >> 4), db,
-                            id | idesc_mx_b_scale(k), tSA, tSB, acc);
+                            id | idesc_mx_b_scale(k), tSA, tSB + 4 * b, acc);
                   acc = 1;
                 }
             }

@@ -110,6 +110,9 @@ class Model:
                 yield self.o_free[(p - 1) & 1], (p - 1) >> 1
             for j in tiles:
                 yield self.p_full[j & 1], j >> 1
+                ahead = j - (1 if "one place for scales" in self.planted else 2)
+                if self.four and ahead >= 0 and self.pv_done[ahead] < self.pv:
+                    raise Fault("scales are copied under the PV GEMM that reads them")
                 q.append([lambda j=j: finish(j), self.empty[j % self.ns].arrive,
                           self.p_free[j & 1].arrive])
             q.append([self.o_full.arrive])
@@ -239,10 +242,12 @@ def test_waits_pass_on_their_own_phase(four, rows):
     (False, 64, "rescale behind one phase", "two before|under the PV"),
     (True, 16, "scores for all warps", "over|no agent"),
     (True, 16, "rope beside place", "two before"),
+    (True, 16, "one place for scales", "scales are copied"),
+    (True, 64, "one place for scales", "scales are copied"),
 ])
 def test_the_model_finds(four, rows, planted, word):
     """Orders that the kernels do not have: a rescale that waits for the last tile alone,
     warps that wait for scores which others free, a place for the rope waited for beside
-    the one in the ring."""
+    the one in the ring, one place for the scales of all tiles."""
     with pytest.raises(Fault, match=word):
         runs(four, rows, 400, (planted,))
