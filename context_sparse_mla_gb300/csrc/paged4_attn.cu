@@ -182,9 +182,10 @@ __device__ __forceinline__ uint2 split_p4(uint32_t x, uint32_t y) {
 // moves when a tile's largest lies kP4Up above it; a sum of 2^30 values stays below
 // 2^(30 + 9 + 80).  A tile's weights lose bits where its largest u lies 72 below the first
 // tile's, and are 0 at 89: in a channel that the heavier tokens have, binary32 holds
-// nothing of them either; in one where those are all zero they are lost.  m never goes down.  (With m 6 below the first
-// tile's largest and moves 28 above it each row moves now and then, and every eighth tile
-// of 64 rows waits for the PV GEMM: 394 us where this takes 257.)
+// nothing of them either; in one where those are all zero they are lost.  m never goes
+// down.  (With m 6 below the first tile's largest and moves 28 above it each row moves now
+// and then, and every eighth tile of 64 rows waits for the PV GEMM: 394 us where this
+// takes 257.)
 constexpr float kP4Over = 40.f, kP4Up = 80.f;
 // What a thread's n keys need in the tiles that few are: those of an open end, with a page
 // that is not there, or with a value of 2^26 and more.  Out of line, as the roles' loops
